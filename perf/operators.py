@@ -11,7 +11,7 @@ float32) and the library's own calls:
             activations and weights in 8 bits
 
 The 8-bit format: 128 values along the contraction share a scale 2^e, e the
-smallest integer with max|v| <= 448 * 2^e (kept in [-120, 119]) and held as the
+smallest integer with max|v| <= 448 * 2^e (kept in [-120, 120]) and held as the
 byte e + 127; a value is its e4m3 code times the scale. Rows are padded with
 zero codes to a multiple of 128 and their scales to a multiple of 16 bytes.
 Expert weights are laid out once for the matrix cores, as
@@ -141,7 +141,7 @@ def _encode(v):
     """float32 rows [..., K] (K a multiple of 128) to (codes [..., K] e4m3, scale bytes [..., K / 128] uint8)."""
     b = v.reshape(*v.shape[:-1], -1, 128)
     m, e = torch.frexp(b.abs().amax(dim=-1))  # max = m 2^e, m in [0.5, 1); 448 = 0.875 2^9
-    e = (e - 9 + (m > 0.875).to(torch.int32)).clamp(-120, 119)
+    e = (e - 9 + (m > 0.875).to(torch.int32)).clamp(-120, 120)
     e = torch.where(m == 0, torch.full_like(e, -120), e)
     codes = torch.ldexp(b, -e.unsqueeze(-1)).to(torch.float8_e4m3fn)
     return codes.reshape(v.shape), (e + 127).to(torch.uint8)
@@ -355,7 +355,7 @@ def _blocks_64(v):
     top = b.abs().amax(dim=-1)
     e = torch.ceil(torch.log2(top / 448.0).clamp(min=-120.0))
     e = torch.where(torch.exp2(e - 1) * 448.0 >= top, e - 1, e)  # should the logarithm have rounded up
-    e = torch.where(torch.exp2(e) * 448.0 < top, e + 1, e).clamp(-120.0, 119.0)
+    e = torch.where(torch.exp2(e) * 448.0 < top, e + 1, e).clamp(-120.0, 120.0)
     scale = torch.exp2(e)
     return _e4m3_64(b / scale[..., None]).reshape(v.shape), scale
 
