@@ -34,4 +34,23 @@ from ._lib import (  # noqa: F401
     moe_status_str,
     moe_workspace_size,
 )
+from ._ext import (  # noqa: F401
+    MOEX_STAGE_BALANCE,
+    MOEX_STAGE_FFN_FP8,
+    MOEX_STAGE_FORWARD_FP8,
+    MOEX_STAGE_NORM_BACKWARD,
+    MOEX_STAGE_TRAIN_BALANCED,
+    code_pitch,
+    expert_shapes,
+    moex_add_rmsnorm,
+    moex_add_rmsnorm_backward,
+    moex_backward_balanced,
+    moex_balance_loss,
+    moex_forward_fp8,
+    moex_grouped_ffn_fp8,
+    moex_quantize_experts,
+    moex_quantize_rows,
+    moex_workspace_size,
+    scale_pitch,
+)
 from .layer import MoEForward  # noqa: F401

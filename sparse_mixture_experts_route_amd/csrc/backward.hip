@@ -31,6 +31,8 @@ __device__ __forceinline__ void bf16x8_to_f32(const u32x4& v, float* f) {
 // One wave per token (k <= 8): dG[j] from the token's dy row and its k
 // expert-output rows, the rows of dYp, then the router's softmax backward
 // over the E logits (lane l owns experts l, l + 64, ...).
+// ADD: dlogit holds another loss's gradient of the logits, which is added.
+template <bool ADD>
 __global__ __launch_bounds__(kBwdWaves * kWave) void bwd_combine_kernel(
     const u32x4* __restrict__ dy, const float* __restrict__ gate, const int32_t* __restrict__ idx,
     const int32_t* __restrict__ inv, const u32x4* __restrict__ Y, const float* __restrict__ logits,
@@ -96,6 +98,7 @@ __global__ __launch_bounds__(kBwdWaves * kWave) void bwd_combine_kernel(
       for (int j = 0; j < 8; ++j)
         if (j < k && idx[t * k + j] == e) dp += dg[j];
       dl = p * (dp - pdp);
+      if (ADD) dl += dlogit[t * E + e];
       dlogit[t * E + e] = dl;
       prob[t * E + e] = p;
     }
@@ -198,12 +201,13 @@ int64_t bwd_stat_chunks(int64_t T) { return ceil_div(T, kStatTokens); }
 
 hipError_t launch_bwd_combine(const moe_problem_t& p, const void* dy, const float* gate, const int32_t* idx,
                               const int32_t* inv, const void* Y_perm, const float* logits, void* dYp,
-                              float* dlogit, bf16_bits* dlogit_b, float* prob, int Ep, hipStream_t s) {
+                              float* dlogit, bf16_bits* dlogit_b, float* prob, int Ep, bool add, hipStream_t s) {
   if (p.k > 8) return hipErrorInvalidValue;
   const int64_t row_vecs = (int64_t)p.d_model * 2 / 16;
-  hipLaunchKernelGGL(bwd_combine_kernel, dim3((unsigned)ceil_div(p.T, kBwdWaves)), dim3(kBwdWaves * kWave), 0, s,
-                     (const u32x4*)dy, gate, idx, inv, (const u32x4*)Y_perm, logits, (u32x4*)dYp, dlogit, dlogit_b,
-                     prob, p.T, p.k, p.E, Ep, row_vecs);
+  hipLaunchKernelGGL(add ? bwd_combine_kernel<true> : bwd_combine_kernel<false>,
+                     dim3((unsigned)ceil_div(p.T, kBwdWaves)), dim3(kBwdWaves * kWave), 0, s, (const u32x4*)dy, gate,
+                     idx, inv, (const u32x4*)Y_perm, logits, (u32x4*)dYp, dlogit, dlogit_b, prob, p.T, p.k, p.E, Ep,
+                     row_vecs);
   return hipGetLastError();
 }
 

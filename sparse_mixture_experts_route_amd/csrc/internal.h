@@ -149,14 +149,40 @@ size_t bwd_partials_bytes(int64_t R, int E, int N);
 // Rows of x^T dlogit per split of the router weight gradient, and the number of splits.
 int bwd_router_splits(int64_t T, int d, int E);
 hipError_t launch_sum_splits(const uint16_t* part, int splits, int64_t n, uint16_t* out, hipStream_t s);
+// With `add`, dlogit holds another loss's gradient of the logits on entry, which is added.
 hipError_t launch_bwd_combine(const moe_problem_t& p, const void* dy, const float* gate, const int32_t* idx,
                               const int32_t* inv, const void* Y_perm, const float* logits, void* dYp,
-                              float* dlogit, uint16_t* dlogit_b, float* prob, int Ep, hipStream_t s);
+                              float* dlogit, uint16_t* dlogit_b, float* prob, int Ep, bool add, hipStream_t s);
 hipError_t launch_bwd_dx(const moe_problem_t& p, const void* dXp, const int32_t* inv, const void* dxr, void* dx,
                          hipStream_t s);
 hipError_t launch_gelu_rows(const void* U, void* H, int64_t elems, hipStream_t s);
 int64_t bwd_stat_chunks(int64_t T);
 hipError_t launch_bwd_stats(const moe_problem_t& p, const float* prob, const float* dlogit, const int32_t* counts,
                             float* part, float* load_frac, float* mean_prob, float* dbias, hipStream_t s);
+
+// ---- operators around the layer (moe_ext.h)
+constexpr int kNormMaxWidth = 32768;  // 1024 threads of 4 pieces of 8 values
+hipError_t launch_add_rmsnorm(const moe_problem_t& p, const void* x, const void* residual, const void* gain, float eps,
+                              void* h, void* y, void* y8, void* y_scale, float* rstd, hipStream_t s);
+// part: norm_bwd_blocks(T, d) * d float32
+int64_t norm_bwd_blocks(int64_t T, int d);
+hipError_t launch_rmsnorm_backward(const moe_problem_t& p, const void* h, const void* gain, const float* rstd,
+                                   const void* dy, const void* dh, void* dx, float* dgain, float* part,
+                                   hipStream_t s);
+hipError_t launch_quantize_rows(const moe_problem_t& p, const void* x, void* x8, void* x_scale, hipStream_t s);
+// ws: balance_ws_ints(p) int32
+size_t balance_ws_ints(const moe_problem_t& p);
+hipError_t launch_balance(const moe_problem_t& p, const float* logits, const int32_t* idx, const uint8_t* mask,
+                          float coef, float* loss, int32_t* counts, float* mean_prob, float* dlogits, int32_t* ws,
+                          hipStream_t s);
+// codes and scales of w [E, K, N] bf16 in the matrix-core layout of moe_ext.h
+hipError_t launch_quantize_weights(const void* w, void* q, void* qs, int E, int K, int N, hipStream_t s);
+// C[r] = A[r] B[e] for rows r of every expert group, 8-bit operands: A codes and
+// scales by rows of K values (row perm[r] of a_rows, or row r), B as
+// launch_quantize_weights writes it. act: C is the 8-bit rows of GELU_tanh
+// (C, Cs), else bf16 [R, N].
+hipError_t launch_gemm_fp8(const void* A, const void* As, const int32_t* perm, int64_t a_rows, const int32_t* offsets,
+                           const void* B, const void* Bs, void* C, void* Cs, int64_t R, int K, int N, int E, bool act,
+                           hipStream_t s);
 
 }  // namespace moe

@@ -7,55 +7,12 @@
 #include <cstring>
 #include <mutex>
 
+#include "api_common.h"
 #include "internal.h"
 
-#define MOE_API extern "C" __attribute__((visibility("default")))
+using namespace moe;
 
 namespace {
-
-constexpr size_t kAlign = 256;
-
-inline bool aligned16(const void* ptr) { return ((uintptr_t)ptr & 15u) == 0; }
-
-inline size_t elem_size(int32_t dtype) { return dtype == MOE_DTYPE_BF16 ? 2 : 4; }
-
-moe_status_t check_problem(const moe_problem_t* p) {
-  if (!p) return MOE_ERR_INVALID_ARGUMENT;
-  if (p->dtype != MOE_DTYPE_F32 && p->dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARGUMENT;
-  if (p->T < 1 || p->E < 1 || p->k < 1 || p->k > p->E || p->d_model < 1 || p->d_expert < 1)
-    return MOE_ERR_INVALID_ARGUMENT;
-  if (p->E > 256) return MOE_ERR_UNSUPPORTED;
-  if (p->T > (int64_t)INT32_MAX / p->k) return MOE_ERR_UNSUPPORTED;
-  if (p->d_model % 64 != 0 || p->d_expert % 64 != 0) return MOE_ERR_UNSUPPORTED;
-  return MOE_OK;
-}
-
-// Sequential sub-allocation of a caller-provided workspace (or size counting when base is null).
-struct Carver {
-  char* base;
-  size_t off = 0;
-  explicit Carver(void* b) : base((char*)b) {}
-  template <typename T>
-  T* take(size_t n) {
-    off = (off + kAlign - 1) / kAlign * kAlign;
-    T* ptr = base ? (T*)(base + off) : nullptr;
-    off += n * sizeof(T);
-    return ptr;
-  }
-};
-
-struct PermuteWs {
-  int32_t* blockcounts;
-  int32_t* blockbase;
-};
-
-PermuteWs carve_permute(Carver& c, const moe_problem_t& p) {
-  const size_t n = (size_t)moe::permute_blocks(p.T) * (size_t)p.E;
-  PermuteWs w;
-  w.blockcounts = c.take<int32_t>(n);
-  w.blockbase = c.take<int32_t>(n);
-  return w;
-}
 
 struct FfnWs {
   void* h;            // hidden activations [T*k, d_expert]
@@ -80,12 +37,6 @@ FfnWs carve_ffn(Carver& c, const moe_problem_t& p) {
                              moe::grouped_gemm_partials_bytes(p.dtype, R, p.d_expert, p.d_model, p.E));
   w.partials = c.take<float>(pb / sizeof(float));
   return w;
-}
-
-// float32 partial logits of a router split over d_model (none when unsplit)
-float* carve_route(Carver& c, const moe_problem_t& p) {
-  const size_t n = moe::route_partials_bytes(p) / sizeof(float);
-  return n ? c.take<float>(n) : nullptr;
 }
 
 struct ForwardWs {
@@ -185,10 +136,6 @@ size_t stage_bytes(const moe_problem_t& p, int32_t stage) {
   }
   return c.off + kAlign;  // slack so a 16-byte aligned base can be rounded up to kAlign
 }
-
-inline char* align_ws(void* ws) { return (char*)(((uintptr_t)ws + kAlign - 1) / kAlign * kAlign); }
-
-inline moe_status_t hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 // The first GEMM reads x rows through perm with 32-bit byte offsets into x
 // (bf16 path only).
@@ -381,9 +328,9 @@ MOE_API moe_status_t moe_forward(const moe_problem_t* p, const void* x, const vo
 }
 
 // Training path: bf16, x addressable by the gathering GEMMs, k <= 8, E a multiple of 8.
-inline bool train_supported(const moe_problem_t& p) {
-  return gather_supported(p) && p.k <= 8 && p.E % 8 == 0;
-}
+bool moe::train_supported(const moe_problem_t& p) { return gather_supported(p) && p.k <= 8 && p.E % 8 == 0; }
+
+size_t moe::train_ws_bytes(const moe_problem_t& p) { return stage_bytes(p, MOE_STAGE_TRAIN); }
 
 MOE_API moe_status_t moe_forward_train(const moe_problem_t* p, const void* x, const void* w_router,
                                        const float* router_bias, const void* W1, const void* W2, void* y, void* ws,
@@ -416,6 +363,54 @@ MOE_API moe_status_t moe_forward_train(const moe_problem_t* p, const void* x, co
   return hip_status(e);
 }
 
+hipError_t moe::run_backward(const moe_problem_t& p, const void* x, const void* w_router, const void* W1,
+                             const void* W2, const void* dy, void* dx, void* dw_router, float* dbias, void* dW1,
+                             void* dW2, float* load_frac, float* mean_prob, void* ws, const BalanceTerm* bal,
+                             hipStream_t s) {
+  Carver c(align_ws(ws));
+  const TrainWs w = carve_train(c, p);
+  const int64_t R = p.T * p.k;
+  const int d = p.d_model, de = p.d_expert, Ep = padded_experts(p);
+  typedef const uint16_t* cb;
+  hipError_t e = hipSuccess;
+  if (bal)  // the balance loss's gradient goes where the router's is then added to it
+    e = moe::launch_balance(p, w.logits, w.idx, bal->mask, bal->coef, bal->loss, bal->counts, bal->mean_prob, w.dlogit,
+                            bal->ws, s);
+  if (e == hipSuccess)
+    e = moe::launch_bwd_combine(p, dy, w.gate, w.idx, w.inv, w.y_perm, w.logits, w.dYp, w.dlogit, w.dlogit_b, w.prob,
+                                Ep, bal != nullptr, s);
+  // dU = (dYp W2_e^T) * GELU_tanh'(U), dX = dU W1_e^T
+  if (e == hipSuccess)
+    e = moe::launch_bwd_gemm_nt((cb)w.dYp, d, w.offsets, R, p.E, (cb)W2, d, (int64_t)de * d, (uint16_t*)w.dU, de,
+                                d, (cb)w.U, nullptr, s);
+  if (e == hipSuccess)
+    e = moe::launch_bwd_gemm_nt((cb)w.dU, de, w.offsets, R, p.E, (cb)W1, de, (int64_t)d * de, (uint16_t*)w.dXp, d,
+                                de, nullptr, w.partials, s);
+  // dW2_e = H^T dYp, dW1_e = x[perm]^T dU over each expert's rows
+  if (e == hipSuccess)
+    e = moe::launch_bwd_gemm_tn((cb)w.H, de, nullptr, R, w.offsets, R, p.E, (cb)w.dYp, d, (uint16_t*)dW2, de, d,
+                                w.partials, s);
+  if (e == hipSuccess)
+    e = moe::launch_bwd_gemm_tn((cb)x, d, w.perm, p.T, w.offsets, R, p.E, (cb)w.dU, de, (uint16_t*)dW1, d, de,
+                                w.partials, s);
+  // router: dx_r = dlogit W_r^T, dW_r = x^T dlogit (one group of T rows)
+  if (e == hipSuccess)
+    e = moe::launch_bwd_gemm_nt(w.dlogit_b, Ep, nullptr, p.T, 1, (cb)w_router, p.E, 0, (uint16_t*)w.dxr, d, Ep,
+                                nullptr, nullptr, s);
+  // x^T dlogit over `splits` equal token ranges (one tile row each would leave
+  // most CUs idle), then the bf16 partial products added in split order
+  const int splits = moe::bwd_router_splits(p.T, d, p.E);
+  if (e == hipSuccess)
+    e = moe::launch_bwd_gemm_tn((cb)x, d, nullptr, p.T, nullptr, p.T, splits, w.dlogit_b, Ep,
+                                splits > 1 ? w.dwr_part : (uint16_t*)dw_router, d, p.E, nullptr, s);
+  if (e == hipSuccess && splits > 1)
+    e = moe::launch_sum_splits(w.dwr_part, splits, (int64_t)d * p.E, (uint16_t*)dw_router, s);
+  if (e == hipSuccess) e = moe::launch_bwd_dx(p, w.dXp, w.inv, w.dxr, dx, s);
+  if (e == hipSuccess && (dbias || load_frac || mean_prob))
+    e = moe::launch_bwd_stats(p, w.prob, w.dlogit, w.counts, w.stat_part, load_frac, mean_prob, dbias, s);
+  return e;
+}
+
 MOE_API moe_status_t moe_backward(const moe_problem_t* p, const void* x, const void* w_router, const void* W1,
                                   const void* W2, const void* dy, void* dx, void* dw_router, float* dbias,
                                   void* dW1, void* dW2, float* load_frac, float* mean_prob, void* ws,
@@ -430,44 +425,8 @@ MOE_API moe_status_t moe_backward(const moe_problem_t* p, const void* x, const v
     return MOE_ERR_INVALID_ARGUMENT;
   if (!train_supported(*p)) return MOE_ERR_UNSUPPORTED;
   if (ws_bytes < stage_bytes(*p, MOE_STAGE_TRAIN)) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  Carver c(align_ws(ws));
-  const TrainWs w = carve_train(c, *p);
-  hipStream_t s = (hipStream_t)stream;
-  const int64_t R = p->T * p->k;
-  const int d = p->d_model, de = p->d_expert, Ep = padded_experts(*p);
-  typedef const uint16_t* cb;
-  hipError_t e = moe::launch_bwd_combine(*p, dy, w.gate, w.idx, w.inv, w.y_perm, w.logits, w.dYp, w.dlogit,
-                                         w.dlogit_b, w.prob, Ep, s);
-  // dU = (dYp W2_e^T) * GELU_tanh'(U), dX = dU W1_e^T
-  if (e == hipSuccess)
-    e = moe::launch_bwd_gemm_nt((cb)w.dYp, d, w.offsets, R, p->E, (cb)W2, d, (int64_t)de * d, (uint16_t*)w.dU, de,
-                                d, (cb)w.U, nullptr, s);
-  if (e == hipSuccess)
-    e = moe::launch_bwd_gemm_nt((cb)w.dU, de, w.offsets, R, p->E, (cb)W1, de, (int64_t)d * de, (uint16_t*)w.dXp, d,
-                                de, nullptr, w.partials, s);
-  // dW2_e = H^T dYp, dW1_e = x[perm]^T dU over each expert's rows
-  if (e == hipSuccess)
-    e = moe::launch_bwd_gemm_tn((cb)w.H, de, nullptr, R, w.offsets, R, p->E, (cb)w.dYp, d, (uint16_t*)dW2, de, d,
-                                w.partials, s);
-  if (e == hipSuccess)
-    e = moe::launch_bwd_gemm_tn((cb)x, d, w.perm, p->T, w.offsets, R, p->E, (cb)w.dU, de, (uint16_t*)dW1, d, de,
-                                w.partials, s);
-  // router: dx_r = dlogit W_r^T, dW_r = x^T dlogit (one group of T rows)
-  if (e == hipSuccess)
-    e = moe::launch_bwd_gemm_nt(w.dlogit_b, Ep, nullptr, p->T, 1, (cb)w_router, p->E, 0, (uint16_t*)w.dxr, d, Ep,
-                                nullptr, nullptr, s);
-  // x^T dlogit over `splits` equal token ranges (one tile row each would leave
-  // most CUs idle), then the bf16 partial products added in split order
-  const int splits = moe::bwd_router_splits(p->T, d, p->E);
-  if (e == hipSuccess)
-    e = moe::launch_bwd_gemm_tn((cb)x, d, nullptr, p->T, nullptr, p->T, splits, w.dlogit_b, Ep,
-                                splits > 1 ? w.dwr_part : (uint16_t*)dw_router, d, p->E, nullptr, s);
-  if (e == hipSuccess && splits > 1)
-    e = moe::launch_sum_splits(w.dwr_part, splits, (int64_t)d * p->E, (uint16_t*)dw_router, s);
-  if (e == hipSuccess) e = moe::launch_bwd_dx(*p, w.dXp, w.inv, w.dxr, dx, s);
-  if (e == hipSuccess && (dbias || load_frac || mean_prob))
-    e = moe::launch_bwd_stats(*p, w.prob, w.dlogit, w.counts, w.stat_part, load_frac, mean_prob, dbias, s);
-  return hip_status(e);
+  return hip_status(run_backward(*p, x, w_router, W1, W2, dy, dx, dw_router, dbias, dW1, dW2, load_frac, mean_prob, ws,
+                                 nullptr, (hipStream_t)stream));
 }
 
 MOE_API moe_status_t moe_plan(const moe_problem_t* p, const int32_t* host_counts, moe_plan_t* plan) {

@@ -1,0 +1,399 @@
+// Root-mean-square norm in front of the layer, with the residual's addition
+// and 8-bit rows, and its backward pass.
+//
+//   h = x + residual (rounded), r = 1 / sqrt(mean(h^2) + eps), y = h r gain
+//   z = h r, a = dy gain: dx = r (a - z mean(a z)) + dh, dgain = sum over tokens of dy z
+//
+// Both directions touch every row once and are bound by HBM. A row stays in
+// the registers of the TPR threads that share it (VPT pieces of 8 values each):
+// it is read once, its sum of squares is reduced, and y, its 8-bit form and h
+// leave from the same registers. 16 neighbouring lanes hold the 128 values of
+// one 8-bit block, so a block's largest magnitude is a reduction within a DPP
+// row. The mean square and r are taken in 64 bits (hidden behind the memory
+// traffic), everything else in float32.
+#include "common.h"
+#include "e4m3.h"
+#include "internal.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kNormThreads = 256;
+
+// 8 consecutive values of a row: one 16-byte piece of bfloat16, two of float32
+template <bool BF16>
+struct Piece8 {
+  u32x4 v[BF16 ? 1 : 2];
+};
+
+template <bool BF16>
+__device__ __forceinline__ Piece8<BF16> load8(const void* base, int64_t piece) {
+  Piece8<BF16> r;
+  const u32x4* p = (const u32x4*)base + piece * (BF16 ? 1 : 2);
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 1 : 2); ++i) r.v[i] = p[i];
+  return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void widen8(const Piece8<BF16>& q, float* f) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    f[i] = BF16 ? ((i & 1) ? __uint_as_float(q.v[0][i / 2] & 0xFFFF0000u) : __uint_as_float(q.v[0][i / 2] << 16))
+                : __uint_as_float(q.v[BF16 ? 0 : i / 4][i % 4]);
+}
+
+// rounds 8 values to the row's type and stores them
+template <bool BF16>
+__device__ __forceinline__ Piece8<BF16> narrow8(const float* f) {
+  Piece8<BF16> r;
+  if constexpr (BF16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.v[0][i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.v[i / 4][i % 4] = __float_as_uint(f[i]);
+  }
+  return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store8(void* base, int64_t piece, const Piece8<BF16>& q) {
+  u32x4* p = (u32x4*)base + piece * (BF16 ? 1 : 2);
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 1 : 2); ++i) p[i] = q.v[i];
+}
+
+// Sum over the TPR threads of a row, the same bits in each of them. `slots`
+// holds one value per wave; a barrier separates two uses.
+template <int TPR, typename S>
+__device__ __forceinline__ S row_sum(S v, S* slots) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
+  if constexpr (TPR > kWave) {
+    const int wave = threadIdx.x / kWave, first = threadIdx.x / TPR * (TPR / kWave);
+    if (threadIdx.x % kWave == 0) slots[wave] = v;
+    __syncthreads();
+    v = 0;
+#pragma unroll
+    for (int i = 0; i < TPR / kWave; ++i) v += slots[first + i];
+  }
+  return v;
+}
+
+template <bool BF16, int TPR, int VPT>
+__global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void add_rmsnorm_kernel(
+    const void* __restrict__ x, const void* __restrict__ residual, const void* __restrict__ gain, float eps,
+    void* __restrict__ h, void* __restrict__ y, uint8_t* __restrict__ y8, uint8_t* __restrict__ y_scale,
+    float* __restrict__ rstd, int64_t T, int nvec, double inv_d) {
+  constexpr int THREADS = TPR > kNormThreads ? TPR : kNormThreads;
+  __shared__ double s_sum[THREADS / kWave];
+  const int j = threadIdx.x % TPR;  // place in the row
+  int64_t t = (int64_t)blockIdx.x * (THREADS / TPR) + threadIdx.x / TPR;
+  const bool live = t < T;
+  if (TPR <= kWave && !live) return;  // a whole wave: no barrier below
+  const int64_t row = (live ? t : T - 1) * nvec;
+  Piece8<BF16> in[VPT], res[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = i * TPR + j;
+    if (c < nvec) {
+      in[i] = load8<BF16>(x, row + c);
+      if (residual) res[i] = load8<BF16>(residual, row + c);
+    }
+  }
+  float v[VPT][8];
+  double ss = 0.0;  // one rounding of r: its error would be every value's of the row
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = i * TPR + j;
+    if (c < nvec) {
+      widen8<BF16>(in[i], v[i]);
+      if (residual) {
+        float b[8];
+        widen8<BF16>(res[i], b);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[i][q] += b[q];
+        in[i] = narrow8<BF16>(v[i]);
+        if (live) store8<BF16>(h, row + c, in[i]);
+        widen8<BF16>(in[i], v[i]);  // the norm is taken of the stored h
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) ss = fma((double)v[i][q], (double)v[i][q], ss);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[i][q] = 0.0f;
+    }
+  }
+  ss = row_sum<TPR>(ss, s_sum);
+  const float r = (float)(1.0 / sqrt(ss * inv_d + (double)eps));
+  if (rstd && live && j == 0) rstd[t] = r;
+  if (!y && !y8) return;  // the same for every thread
+  const int64_t cp = code_pitch((int64_t)nvec * 8), sp = scale_pitch((int64_t)nvec * 8);
+  const int kb = (int)(cp / kQBlock);
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = i * TPR + j;
+    if (c < nvec) {
+      float g[8];
+      widen8<BF16>(load8<BF16>(gain, c), g);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[i][q] = v[i][q] * r * g[q];
+      if (y && live) store8<BF16>(y, row + c, narrow8<BF16>(v[i]));
+    }
+    if (y8) {
+      float m = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) m = fmaxf(m, fabsf(v[i][q]));
+      const int byte = scale_byte(row16_max(m));  // the lanes of a block: pieces 16 b .. 16 b + 15
+      const float inv = inv_scale(byte);
+      u32x2 o;
+      o[0] = encode4(v[i][0], v[i][1], v[i][2], v[i][3], inv);
+      o[1] = encode4(v[i][4], v[i][5], v[i][6], v[i][7], inv);
+      if (live && c < kb * 16) {  // a last half block ends in zero codes
+        *(u32x2*)(y8 + t * cp + (int64_t)c * 8) = o;
+        if (c % 16 == 0) y_scale[t * sp + c / 16] = (uint8_t)byte;
+      }
+    }
+  }
+  if (y8 && live && kb + j < sp) y_scale[t * sp + kb + j] = 0;
+}
+
+// 8-bit rows of x alone: one thread per piece of 8 values
+template <bool BF16>
+__global__ __launch_bounds__(256) void quantize_rows_kernel(const void* __restrict__ x, uint8_t* __restrict__ x8,
+                                                            uint8_t* __restrict__ x_scale, int64_t T, int nvec) {
+  const int64_t cp = code_pitch((int64_t)nvec * 8), sp = scale_pitch((int64_t)nvec * 8);
+  const int pv = (int)(cp / 8);  // pieces per padded row, a multiple of 16
+  const int64_t n = T * pv;
+  for (int64_t i0 = (int64_t)blockIdx.x * 256; i0 < n; i0 += (int64_t)gridDim.x * 256) {
+    const int64_t i = i0 + threadIdx.x, t = min(i, n - 1) / pv;
+    const int c = (int)(i - t * pv);
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (i < n && c < nvec) widen8<BF16>(load8<BF16>(x, t * nvec + c), v);
+    float m = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) m = fmaxf(m, fabsf(v[q]));
+    const int byte = scale_byte(row16_max(m));
+    const float inv = inv_scale(byte);
+    u32x2 o;
+    o[0] = encode4(v[0], v[1], v[2], v[3], inv);
+    o[1] = encode4(v[4], v[5], v[6], v[7], inv);
+    if (i < n) {
+      *(u32x2*)(x8 + i * 8) = o;
+      if (c % 16 == 0) x_scale[t * sp + c / 16] = (uint8_t)byte;
+      // the bytes past the last block, written by the row's first pieces
+      for (int q = pv / 16 + c; c < 16 && q < sp; q += 16) x_scale[t * sp + q] = 0;
+    }
+  }
+}
+
+// A block takes rows blockIdx, blockIdx + gridDim, ... of its row groups and
+// keeps its share of dgain in registers; the row groups of the block are then
+// added through LDS and leave as one float32 row of `part`.
+template <bool BF16, int TPR, int VPT>
+__global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void rmsnorm_backward_kernel(
+    const void* __restrict__ h, const void* __restrict__ gain, const float* __restrict__ rstd,
+    const void* __restrict__ dy, const void* __restrict__ dh, void* __restrict__ dx, float* __restrict__ part,
+    int64_t T, int nvec, float inv_d) {
+  constexpr int THREADS = TPR > kNormThreads ? TPR : kNormThreads;
+  constexpr int RPB = THREADS / TPR;
+  __shared__ float s_sum[2][THREADS / kWave];
+  __shared__ float s_acc[RPB > 1 ? TPR * VPT * 8 : 1];
+  const int j = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+  float acc[VPT][8];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) acc[i][q] = 0.0f;
+  int turn = 0;
+  for (int64_t t0 = (int64_t)blockIdx.x * RPB; t0 < T; t0 += (int64_t)gridDim.x * RPB, turn ^= 1) {
+    const int64_t t = t0 + grp;
+    const bool live = t < T;  // a row group past the end adds zeros and stores nothing
+    const int64_t row = t * nvec;
+    const float r = live ? rstd[t] : 0.0f;
+    Piece8<BF16> ph[VPT], pd[VPT], pr[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = i * TPR + j;
+      ph[i] = Piece8<BF16>{};
+      pd[i] = Piece8<BF16>{};
+      pr[i] = Piece8<BF16>{};
+      if (live && c < nvec) {
+        ph[i] = load8<BF16>(h, row + c);
+        pd[i] = load8<BF16>(dy, row + c);
+        if (dh) pr[i] = load8<BF16>(dh, row + c);
+      }
+    }
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = i * TPR + j;
+      if (c < nvec) {
+        float z[8], d[8], g[8];
+        widen8<BF16>(ph[i], z);
+        widen8<BF16>(pd[i], d);
+        widen8<BF16>(load8<BF16>(gain, c), g);
+        float p = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const float zz = z[q] * r;
+          acc[i][q] = fmaf(d[q], zz, acc[i][q]);
+          p = fmaf(d[q] * g[q], zz, p);
+        }
+        s += p;
+      }
+    }
+    // two sets of slots in turn: a wave may be one row ahead of the slowest reader
+    s = row_sum<TPR>(s, s_sum[turn]) * inv_d;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = i * TPR + j;
+      if (live && c < nvec) {
+        float z[8], d[8], g[8], o[8];
+        widen8<BF16>(ph[i], z);
+        widen8<BF16>(pd[i], d);
+        widen8<BF16>(load8<BF16>(gain, c), g);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) o[q] = r * (d[q] * g[q] - z[q] * r * s);
+        if (dh) {
+          float e[8];
+          widen8<BF16>(pr[i], e);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) o[q] += e[q];
+        }
+        store8<BF16>(dx, row + c, narrow8<BF16>(o));
+      }
+    }
+  }
+  // the block's row groups in order
+  if constexpr (RPB > 1) {
+    for (int u = 1; u < RPB; ++u) {
+      __syncthreads();
+      if (grp == u)
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+          for (int q = 0; q < 8; ++q) s_acc[(i * 8 + q) * TPR + j] = acc[i][q];
+      __syncthreads();
+      if (grp == 0)
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+          for (int q = 0; q < 8; ++q) acc[i][q] += s_acc[(i * 8 + q) * TPR + j];
+    }
+  }
+  if (grp == 0) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = i * TPR + j;
+      if (c < nvec) {
+        f32x4* p = (f32x4*)(part + ((int64_t)blockIdx.x * nvec + c) * 8);
+        p[0] = f32x4{acc[i][0], acc[i][1], acc[i][2], acc[i][3]};
+        p[1] = f32x4{acc[i][4], acc[i][5], acc[i][6], acc[i][7]};
+      }
+    }
+  }
+}
+
+// dgain: 64 columns per block, 16 slices of the partial rows added side by
+// side and then in slice order
+constexpr int kDgSlices = 16;
+__global__ __launch_bounds__(64 * kDgSlices) void dgain_kernel(const float* __restrict__ part,
+                                                               float* __restrict__ dgain, int rows, int d) {
+  __shared__ float s_v[kDgSlices][64];
+  const int c = threadIdx.x % 64, sl = threadIdx.x / 64;
+  const int col = blockIdx.x * 64 + c;  // d is a multiple of 64
+  float a = 0.0f;
+#pragma unroll 4
+  for (int i = sl; i < rows; i += kDgSlices) a += part[(int64_t)i * d + col];
+  s_v[sl][c] = a;
+  __syncthreads();
+  if (sl == 0) {
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kDgSlices; ++i) v += s_v[i][c];
+    dgain[col] = v;
+  }
+}
+
+// Threads per row and pieces per thread by row width (pieces of 8 values).
+#define MOE_NORM_SHAPES(F)                                                                              \
+  if (nvec <= 64) { F(64, 1); }                                                                         \
+  else if (nvec <= 128) { F(64, 2); }                                                                   \
+  else if (nvec <= 256) { F(64, 4); }                                                                   \
+  else if (nvec <= 512) { F(128, 4); }                                                                  \
+  else if (nvec <= 1024) { F(256, 4); }                                                                 \
+  else if (nvec <= 2048) { F(512, 4); }                                                                 \
+  else { F(1024, 4); }
+
+int rows_per_block(int nvec) { return nvec <= 256 ? 4 : nvec <= 512 ? 2 : 1; }
+
+}  // namespace
+
+// Blocks of the backward launch, and rows of partial sums
+int64_t norm_bwd_blocks(int64_t T, int d) {
+  return min(ceil_div(T, rows_per_block(d / 8)), (int64_t)512);
+}
+
+hipError_t launch_add_rmsnorm(const moe_problem_t& p, const void* x, const void* residual, const void* gain, float eps,
+                              void* h, void* y, void* y8, void* y_scale, float* rstd, hipStream_t s) {
+  const int nvec = p.d_model / 8;
+  const int64_t blocks = ceil_div(p.T, rows_per_block(nvec));
+  const double inv_d = 1.0 / p.d_model;
+  if (p.d_model > kNormMaxWidth || blocks > INT32_MAX) return hipErrorInvalidValue;
+#define MOE_NORM(TPR, VPT)                                                                                      \
+  do {                                                                                                          \
+    const dim3 b(TPR > kNormThreads ? TPR : kNormThreads);                                                      \
+    if (p.dtype == MOE_DTYPE_BF16)                                                                              \
+      hipLaunchKernelGGL((add_rmsnorm_kernel<true, TPR, VPT>), dim3((unsigned)blocks), b, 0, s, x, residual, gain, \
+                         eps, h, y, (uint8_t*)y8, (uint8_t*)y_scale, rstd, p.T, nvec, inv_d);                   \
+    else                                                                                                        \
+      hipLaunchKernelGGL((add_rmsnorm_kernel<false, TPR, VPT>), dim3((unsigned)blocks), b, 0, s, x, residual,   \
+                         gain, eps, h, y, (uint8_t*)y8, (uint8_t*)y_scale, rstd, p.T, nvec, inv_d);             \
+  } while (0)
+  MOE_NORM_SHAPES(MOE_NORM)
+#undef MOE_NORM
+  return hipGetLastError();
+}
+
+hipError_t launch_rmsnorm_backward(const moe_problem_t& p, const void* h, const void* gain, const float* rstd,
+                                   const void* dy, const void* dh, void* dx, float* dgain, float* part,
+                                   hipStream_t s) {
+  const int nvec = p.d_model / 8;
+  if (p.d_model > kNormMaxWidth) return hipErrorInvalidValue;
+  const int64_t blocks = norm_bwd_blocks(p.T, p.d_model);
+  const float inv_d = 1.0f / (float)p.d_model;
+#define MOE_NORM(TPR, VPT)                                                                                       \
+  do {                                                                                                           \
+    const dim3 b(TPR > kNormThreads ? TPR : kNormThreads);                                                       \
+    if (p.dtype == MOE_DTYPE_BF16)                                                                               \
+      hipLaunchKernelGGL((rmsnorm_backward_kernel<true, TPR, VPT>), dim3((unsigned)blocks), b, 0, s, h, gain,    \
+                         rstd, dy, dh, dx, part, p.T, nvec, inv_d);                                              \
+    else                                                                                                         \
+      hipLaunchKernelGGL((rmsnorm_backward_kernel<false, TPR, VPT>), dim3((unsigned)blocks), b, 0, s, h, gain,   \
+                         rstd, dy, dh, dx, part, p.T, nvec, inv_d);                                              \
+  } while (0)
+  MOE_NORM_SHAPES(MOE_NORM)
+#undef MOE_NORM
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(dgain_kernel, dim3((unsigned)(p.d_model / 64)), dim3(64 * kDgSlices), 0, s, (const float*)part,
+                     dgain, (int)blocks, p.d_model);
+  return hipGetLastError();
+}
+
+hipError_t launch_quantize_rows(const moe_problem_t& p, const void* x, void* x8, void* x_scale, hipStream_t s) {
+  const int64_t n = p.T * (code_pitch(p.d_model) / 8);
+  const int64_t blocks = min(ceil_div(n, 256), (int64_t)65536);
+  if (p.dtype == MOE_DTYPE_BF16)
+    hipLaunchKernelGGL(quantize_rows_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, s, x, (uint8_t*)x8,
+                       (uint8_t*)x_scale, p.T, p.d_model / 8);
+  else
+    hipLaunchKernelGGL(quantize_rows_kernel<false>, dim3((unsigned)blocks), dim3(256), 0, s, x, (uint8_t*)x8,
+                       (uint8_t*)x_scale, p.T, p.d_model / 8);
+  return hipGetLastError();
+}
+
+}  // namespace moe
