@@ -9,6 +9,11 @@ namespace moe {
 
 constexpr int kQBlock = 128;  // values per scale
 
+template <int V>
+struct IntC {
+  static constexpr int value = V;
+};
+
 __host__ __device__ __forceinline__ int64_t code_pitch(int64_t K) { return (K + 127) / 128 * 128; }
 __host__ __device__ __forceinline__ int64_t scale_pitch(int64_t K) { return (K + 2047) / 2048 * 16; }
 

@@ -21,7 +21,10 @@
 
 #include "common.h"
 #include "e4m3.h"
+#include "gemm_lanes.h"
 #include "internal.h"
+#include "lds_dma.h"
+#include "tiles.h"
 
 namespace moe {
 
@@ -29,7 +32,7 @@ namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-__device__ __forceinline__ i32x8 join8(const u32x4& a, const u32x4& b) {
+__device__ __forceinline__ i32x8 join8(u32x4 a, u32x4 b) {
   return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
 
@@ -208,6 +211,377 @@ __global__ __launch_bounds__(NG * KS * kWave) void gemm_fp8_small_kernel(
   }
 }
 
+// ---- 256 x 256 tiles of large groups
+//
+// Eight waves of 64 x 128 (two per SIMD: one multiplies while the other issues
+// loads), a step of 128 positions, two LDS stages of 64 KB filled by direct
+// loads, persistent workgroups over the tile list of tiles.h. A sits
+// row-major in LDS with the 16-byte piece index XOR-ed by (row >> 1) & 7, so
+// the 16 lanes served together touch every bank once; a stage of B is a
+// straight copy of the weight layout, in which a wave's fragment read is 1 KB
+// in lane order. The scales of 16 steps, 16 bytes a row, are one load per wave
+// and come in two windows used in turn. A fragment of B is read again as soon
+// as the two instructions that use it are issued, so only A needs two register
+// sets: 192 of the 256 registers that two waves per SIMD leave hold operands
+// and sums.
+constexpr int L_BM = 256, L_BN = 256, L_NW = 8, L_WN = 2, L_TM = 2, L_TN = 4;
+constexpr int L_A = L_BM * kQBlock, L_B = L_BN * kQBlock, L_STAGE = L_A + L_B;
+constexpr int L_WIN = 8192;       // 16 steps' scales of 256 rows and 256 columns
+constexpr int L_NL = L_STAGE / 1024 / L_NW;  // loads per wave and stage
+constexpr int L_ALD = L_NL / 2;
+
+template <bool ACT, bool GATHER>
+__global__ __launch_bounds__(L_NW * kWave, 1) void gemm_fp8_kernel(
+    const uint8_t* __restrict__ A, const uint8_t* __restrict__ As, const int32_t* __restrict__ perm, int64_t a_rows,
+    const int32_t* __restrict__ offsets, const uint8_t* __restrict__ B, const uint8_t* __restrict__ Bs,
+    void* __restrict__ C, uint8_t* __restrict__ Cs, int64_t R, int K, int N, int E, int n_tiles, int gm) {
+  __shared__ __attribute__((aligned(1024))) char smem[2 * L_STAGE + 2 * L_WIN];
+  __shared__ int s_tstart[257];
+  __shared__ int s_mtiles[256];
+  const int tid = threadIdx.x, lane = tid % kWave, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  build_tile_list<L_BM>(offsets, E, R, n_tiles, s_tstart, s_mtiles);
+  const int total = s_tstart[E];
+  const int xcd = blockIdx.x % 8, nb = gridDim.x / 8, j = blockIdx.x / 8;
+  const int lo = (int)((int64_t)total * xcd / 8), hi = (int)((int64_t)total * (xcd + 1) / 8);
+  const int n_items = hi - lo > j ? (hi - lo - j - 1) / nb + 1 : 0;
+  const int cp = (int)code_pitch(K), sp = (int)scale_pitch(K), KB = cp / kQBlock;
+  lds_char* const lds = (lds_char*)smem;
+  const uint32_t lds_base = lds_addr(smem);
+  const int wm0 = (wave / L_WN) * (L_TM * 32), wn0 = (wave % L_WN) * (L_TN * 32);
+
+  struct Tile {
+    int e, n0;
+    int64_t row0, row_end;
+  };
+  struct Loads {
+    i32x4 rsA, rsB, rsS;
+    uint32_t ga[L_ALD], gs, gb;  // this lane's byte offsets of the A, scale and B loads
+  };
+  // the rows of this lane's A pieces and scale load (waves 0 .. 3 load the rows' scales, 4 .. 7 the columns')
+  int a_row[L_ALD], a_c16[L_ALD];
+#pragma unroll
+  for (int i = 0; i < L_ALD; ++i) {
+    const lanes::Piece pc = lanes::a_piece<64>((wave * L_ALD + i) * 64 + lane);  // 128-byte rows
+    a_row[i] = pc.row;
+    a_c16[i] = pc.c * 16;
+  }
+  const int s_row = (wave & 3) * 64 + lane;
+  auto locate = [&](int t) {
+    int a0 = 0, a1 = E;
+    while (a1 - a0 > 1) {
+      const int mid = (a0 + a1) >> 1;
+      if (s_tstart[mid] <= t) a0 = mid; else a1 = mid;
+    }
+    Tile tl;
+    tl.e = __builtin_amdgcn_readfirstlane(a0);
+    const int local = t - __builtin_amdgcn_readfirstlane(s_tstart[tl.e]);
+    const int mt = __builtin_amdgcn_readfirstlane(s_mtiles[tl.e]);
+    int n_tile, m_idx;
+    tile_coords(local, mt, n_tiles, gm, n_tile, m_idx);
+    tl.row0 = (int64_t)max(__builtin_amdgcn_readfirstlane(offsets[tl.e]), 0) + (int64_t)m_idx * L_BM;
+    tl.row_end = min((int64_t)__builtin_amdgcn_readfirstlane(offsets[tl.e + 1]), R);
+    tl.n0 = n_tile * L_BN;
+    return tl;
+  };
+  auto load_perm = [&](const Tile& t_, int (&pv)[L_ALD + 1]) {
+#pragma unroll
+    for (int i = 0; i <= L_ALD; ++i) {
+      const int64_t r = t_.row0 + (i < L_ALD ? a_row[i < L_ALD ? i : 0] : s_row);
+      pv[i] = r < t_.row_end ? perm[r] : -1;
+    }
+  };
+  auto bind = [&](const Tile& t_, const int (&pv)[L_ALD + 1]) {
+    Loads l;
+    const int rows = (int)min(t_.row_end - t_.row0, (int64_t)L_BM);
+    l.rsA = GATHER ? buffer_rsrc(A, (uint32_t)(a_rows * cp)) : buffer_rsrc(A + t_.row0 * cp, (uint32_t)(rows * cp));
+    l.rsB = buffer_rsrc(B + (int64_t)t_.e * N * cp, (uint32_t)((int64_t)N * cp));
+    if (wave < 4)
+      l.rsS = GATHER ? buffer_rsrc(As, (uint32_t)(a_rows * sp)) : buffer_rsrc(As + t_.row0 * sp, (uint32_t)(rows * sp));
+    else
+      l.rsS = buffer_rsrc(Bs + (int64_t)t_.e * N * KB, (uint32_t)((int64_t)N * KB));
+#pragma unroll
+    for (int i = 0; i <= L_ALD; ++i) {
+      const int row = i < L_ALD ? a_row[i < L_ALD ? i : 0] : s_row;
+      const int src = GATHER ? pv[i] : row;  // past the group's end: -1, or past the descriptor's range
+      const bool ok = src >= 0 && (!GATHER || src < a_rows);
+      if (i < L_ALD)
+        l.ga[i] = ok ? (uint32_t)src * (uint32_t)cp + a_c16[i < L_ALD ? i : 0] : lanes::kOutOfRange;
+      else
+        l.gs = ok ? (uint32_t)src * (uint32_t)sp : lanes::kOutOfRange;
+    }
+    const int g = t_.n0 / 32 + wave;  // this wave's column group of the stage
+    l.gb = g * 32 < N ? (uint32_t)g * (uint32_t)(KB * 4096) + lane * 16 : lanes::kOutOfRange;
+    if (wave >= 4) {
+      const int sg = t_.n0 / 32 + (wave - 4) * 2 + half;
+      l.gs = sg * 32 < N ? (uint32_t)sg * (uint32_t)(KB * 32) + (lane & 31) * 16 : lanes::kOutOfRange;
+    }
+    return l;
+  };
+  // the scales of steps 16 w .. 16 w + 15
+  auto issue_window = [&](const Loads& l, int w) {
+    buffer_load_lds16(l.rsS, l.gs, (uint32_t)w * (wave < 4 ? 16u : 512u),
+                      lds_base + 2 * L_STAGE + (w & 1) * L_WIN + wave * 1024);
+  };
+  // load `i` of step kt's stage into ring buffer kt & 1
+  auto issue_one = [&](const Loads& l, int kt, int i) {
+    if (i < L_ALD)
+      buffer_load_lds16(l.rsA, l.ga[i], (uint32_t)kt * kQBlock,
+                        lds_base + (kt & 1) * L_A + (wave * L_ALD + i) * 1024);
+    else
+      buffer_load_lds16(l.rsB, l.gb, (uint32_t)kt * 4096u + (i - L_ALD) * 1024u,
+                        lds_base + 2 * L_A + (kt & 1) * L_B + wave * 4096 + (i - L_ALD) * 1024);
+  };
+
+  i32x8 fa[2][L_TM], fb[L_TN];
+  int sa = 0, sb = 0, sa_n[L_TM], sb_n[L_TN];  // the scale bytes of a step, one per byte
+  f32x16 acc[L_TM][L_TN];
+  typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+  typedef __attribute__((address_space(3))) uint8_t lds_u8;
+  // LDS addresses of this lane's fragment pieces in the buffer being read: both
+  // operands' buffers are L_A apart, so a step moves them all by +-L_A
+  static_assert(L_A == L_B, "one distance moves both operands' addresses");
+  uint32_t ra[4], rb;
+  auto first_addresses = [&]() {
+    const int sw = ((lane & 31) >> 1) & 7;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) ra[q] = lds_base + (wm0 + (lane & 31)) * kQBlock + (((2 * q + half) ^ sw) << 4);
+    rb = lds_base + 2 * L_A + wn0 * kQBlock + lane * 16;
+  };
+  auto move_addresses = [&](int kt) {  // to the buffer of step kt
+    const uint32_t d = (kt & 1) ? (uint32_t)L_A : (uint32_t)-L_A;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) asm("v_add_u32 %0, %0, %1" : "+v"(ra[q]) : "s"(d));
+    asm("v_add_u32 %0, %0, %1" : "+v"(rb) : "s"(d));
+  };
+  auto read_a = [&](int js, int mi) {
+    fa[js][mi] = join8(*(lds_u32x4*)(uintptr_t)(ra[2 * js] + mi * (32 * kQBlock)),
+                       *(lds_u32x4*)(uintptr_t)(ra[2 * js + 1] + mi * (32 * kQBlock)));
+  };
+  auto read_b = [&](int js, int ni) {
+    fb[ni] = join8(*(lds_u32x4*)(uintptr_t)(rb + ni * 4096 + js * 2048),
+                   *(lds_u32x4*)(uintptr_t)(rb + ni * 4096 + js * 2048 + 1024));
+  };
+  auto read_scales = [&](int kt) {
+    lds_char* w = lds + 2 * L_STAGE + ((kt >> 4) & 1) * L_WIN + (kt & 15);
+#pragma unroll
+    for (int mi = 0; mi < L_TM; ++mi) sa_n[mi] = *(lds_u8*)(w + (wm0 + (lane & 31)) * 16 + mi * 512);
+    w += 31 * (kt & 15);
+#pragma unroll
+    for (int ni = 0; ni < L_TN; ++ni) sb_n[ni] = *(lds_u8*)(w + 4096 + wn0 * 16 + (lane & 31) + ni * 512);
+  };
+  auto take_scales = [&]() {
+    sa = sa_n[0] | sa_n[1] << 8;
+    sb = sb_n[0] | sb_n[1] << 8 | sb_n[2] << 16 | sb_n[3] << 24;
+  };
+  auto mfma = [&](int js, auto mi_c, auto ni_c) {
+    constexpr int mi = decltype(mi_c)::value, ni = decltype(ni_c)::value;
+    acc[mi][ni] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[ni], fa[js][mi], acc[mi][ni], 0, 0, ni, sb, mi, sa);
+  };
+  auto mfma_pair = [&](int js, int ni, auto after) {
+    auto two = [&](auto ni_c) {
+      mfma(js, IntC<0>{}, ni_c);
+      after(0);
+      __builtin_amdgcn_sched_barrier(0);
+      mfma(js, IntC<1>{}, ni_c);
+      after(1);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    if (ni == 0) two(IntC<0>{});
+    else if (ni == 1) two(IntC<1>{});
+    else if (ni == 2) two(IntC<2>{});
+    else two(IntC<3>{});
+  };
+  // One step of 128 positions. MORE: another step follows (its stage has to have
+  // landed, and its first fragments are read here); REFILL: step kt + 2 is
+  // loaded into the buffer that this step leaves.
+  auto step = [&](const Loads& l, int kt, auto more_c, auto refill_c) {
+    constexpr bool MORE = decltype(more_c)::value, REFILL = decltype(refill_c)::value;
+#pragma unroll
+    for (int ni = 0; ni < L_TN; ++ni)
+      mfma_pair(0, ni, [&](int mi) {
+        if (ni == 0) read_a(1, mi);
+        if (mi == 1) read_b(1, ni);
+      });
+#pragma unroll
+    for (int ni = 0; ni < L_TN / 2; ++ni) mfma_pair(1, ni, [](int) {});
+    if constexpr (MORE) {
+      wait_vmem<0>();   // step kt + 1 has landed
+      __syncthreads();  // for every wave, and every wave is done reading this buffer
+      move_addresses(kt + 1);
+      read_scales(kt + 1);
+#pragma unroll
+      for (int mi = 0; mi < L_TM; ++mi) read_a(0, mi);
+#pragma unroll
+      for (int ni = 0; ni < L_TN / 2; ++ni) read_b(0, ni);
+    }
+#pragma unroll
+    for (int ni = L_TN / 2; ni < L_TN; ++ni)
+      mfma_pair(1, ni, [&](int mi) {
+        if (MORE && mi == 1) read_b(0, ni);
+        if constexpr (REFILL) {
+          const int at = (ni - L_TN / 2) * L_TM + mi;  // 0 .. 3: two loads each
+          issue_one(l, kt + 2, 2 * at);
+          issue_one(l, kt + 2, 2 * at + 1);
+        }
+      });
+    if constexpr (MORE) take_scales();
+  };
+
+  Tile tl;
+  Loads ld;
+  if (n_items > 0) {
+    tl = locate(lo + j);
+    int pv[L_ALD + 1];
+    if constexpr (GATHER) load_perm(tl, pv);
+    ld = bind(tl, pv);
+    issue_window(ld, 0);
+#pragma unroll
+    for (int i = 0; i < L_NL; ++i) issue_one(ld, 0, i);
+    if (KB > 1)
+#pragma unroll
+      for (int i = 0; i < L_NL; ++i) issue_one(ld, 1, i);
+  }
+  // memory operations issued after an item's stage 0 (each is issued whatever its lanes hold)
+  constexpr int EP_ST = ACT ? 8 + L_TM : 16;
+  int pend = KB > 1 ? L_NL : 0;
+
+  for (int item = 0; item < n_items; ++item) {
+    if (pend == 0) wait_vmem<0>();
+    else if (pend == L_NL) wait_vmem<L_NL>();
+    else if (pend == EP_ST) wait_vmem<EP_ST>();
+    else wait_vmem<EP_ST + L_NL>();
+    __syncthreads();
+    const bool has_next = item + 1 < n_items;
+    Tile nxt = tl;
+    int npv[L_ALD + 1];
+    if (has_next) {
+      nxt = locate(lo + j + (item + 1) * nb);
+      if constexpr (GATHER) load_perm(nxt, npv);
+    }
+#pragma unroll
+    for (int mi = 0; mi < L_TM; ++mi)
+#pragma unroll
+      for (int ni = 0; ni < L_TN; ++ni)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[mi][ni][v] = 0.0f;
+    if (tl.row_end - tl.row0 > wm0) {
+      read_scales(0);
+      take_scales();
+      first_addresses();
+#pragma unroll
+      for (int mi = 0; mi < L_TM; ++mi) read_a(0, mi);
+#pragma unroll
+      for (int ni = 0; ni < L_TN; ++ni) read_b(0, ni);
+      for (int w = 0; 16 * w < KB - 2; ++w) {
+        // the next window goes out with this one's first step: the window before this one is read no more
+        if (16 * (w + 1) < KB) issue_window(ld, w + 1);
+        for (int kt = 16 * w; kt < min(16 * (w + 1), KB - 2); ++kt) step(ld, kt, BoolC<true>{}, BoolC<true>{});
+      }
+      if (KB > 1) step(ld, KB - 2, BoolC<true>{}, BoolC<false>{});
+      step(ld, KB - 1, BoolC<false>{}, BoolC<false>{});
+    } else {
+      // all of this wave's rows lie past the group's end: only its share of the loads
+      for (int kt = 0; kt < KB - 1; ++kt) {
+        if ((kt & 15) == 0 && kt + 16 < KB) issue_window(ld, (kt >> 4) + 1);
+        wait_vmem<0>();
+        __syncthreads();
+        if (kt + 2 < KB) {
+#pragma unroll
+          for (int i = 0; i < L_NL; ++i) issue_one(ld, kt + 2, i);
+        }
+      }
+    }
+    __syncthreads();  // every wave is done with every buffer
+
+    // the next item's first stage goes out before this item's epilogue, which works in buffer 1
+    if (has_next) {
+      ld = bind(nxt, npv);
+      issue_window(ld, 0);
+#pragma unroll
+      for (int i = 0; i < L_NL; ++i) issue_one(ld, 0, i);
+    }
+    lds_char* const ep = lds + (wave < 4 ? L_A : 2 * L_A + L_B - 4 * 8192) + wave * 8192;  // buffer 1 of A, then of B
+    typedef __attribute__((address_space(3))) uint32_t lds_u32;
+    typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
+    const int rows = (int)min(tl.row_end - tl.row0, (int64_t)L_BM);
+    if constexpr (ACT) {
+      const int hp = (int)code_pitch(N), hs = (int)scale_pitch(N);
+      const __amdgpu_buffer_rsrc_t rsC = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)((uint8_t*)C + tl.row0 * hp), (short)0, rows * hp, kBufferFlags);
+      const __amdgpu_buffer_rsrc_t rsCs =
+          __builtin_amdgcn_make_buffer_rsrc((void*)(Cs + tl.row0 * hs), (short)0, rows * hs, kBufferFlags);
+      const int col = tl.n0 + wn0;
+      const bool cols = col < hp;
+#pragma unroll
+      for (int mi = 0; mi < L_TM; ++mi) {
+        float m = 0.0f;
+#pragma unroll
+        for (int ni = 0; ni < L_TN; ++ni)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            acc[mi][ni][v] = gelu_tanh(acc[mi][ni][v]);
+            m = fmaxf(m, fabsf(acc[mi][ni][v]));
+          }
+        m = fmaxf(m, __shfl_xor(m, 32, kWave));
+        const int byte = scale_byte(m);
+        const float inv = inv_scale(byte);
+        const int row = mi * 32 + (lane & 31);
+#pragma unroll
+        for (int ni = 0; ni < L_TN; ++ni)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int ch = ni * 2 + (v >> 1);
+            *(lds_u32*)(ep + row * 128 + ((ch ^ (row & 7)) << 4) + (v & 1) * 8 + half * 4) =
+                encode4(acc[mi][ni][4 * v], acc[mi][ni][4 * v + 1], acc[mi][ni][4 * v + 2], acc[mi][ni][4 * v + 3], inv);
+          }
+        __builtin_amdgcn_raw_buffer_store_b8((uint8_t)byte, rsCs,
+                                             cols && half == 0 ? (wm0 + row) * hs + col / kQBlock : 0x7FFFFFF0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int it = 0; it < 8; ++it) {
+        const int row = it * 8 + lane / 8, ch = lane % 8;
+        const u32x4 v = *(lds_u32x4*)(ep + row * 128 + ((ch ^ (row & 7)) << 4));
+        __builtin_amdgcn_raw_buffer_store_b128(v, rsC, cols ? (wm0 + row) * hp + col + ch * 16 : 0x7FFFFFF0, 0, 0);
+      }
+    } else {
+      const __amdgpu_buffer_rsrc_t rsC = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)((bf16_bits*)C + tl.row0 * N), (short)0, rows * N * 2, kBufferFlags);
+#pragma unroll
+      for (int mi = 0; mi < L_TM; ++mi) {
+#pragma unroll
+        for (int ni = 0; ni < L_TN; ++ni)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            u32x2 o;
+            o[0] = pack_bf16x2(acc[mi][ni][4 * v], acc[mi][ni][4 * v + 1]);
+            o[1] = pack_bf16x2(acc[mi][ni][4 * v + 2], acc[mi][ni][4 * v + 3]);
+            const int row = lane & 31, ch = ni * 4 + v;  // 32 rows of 256 bytes, 16 pieces
+            *(lds_u32x2*)(ep + row * 256 + ((ch ^ (row & 15)) << 4) + half * 8) = o;
+          }
+        // a wave's LDS operations complete in order: no barrier before its own reads
+#pragma unroll
+        for (int it = 0; it < 8; ++it) {
+          const int row = it * 4 + lane / 16, ch = lane % 16;
+          const u32x4 v = *(lds_u32x4*)(ep + row * 256 + ((ch ^ (row & 15)) << 4));
+          const int n = tl.n0 + wn0 + ch * 8;
+          __builtin_amdgcn_raw_buffer_store_b128(v, rsC, lanes::c_store_off(wm0 + mi * 32 + row, n, N), 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    if (has_next) {
+      __syncthreads();  // every wave has read its piece of buffer 1
+      if (KB > 1)
+#pragma unroll
+        for (int i = 0; i < L_NL; ++i) issue_one(ld, 1, i);
+      pend = EP_ST + (KB > 1 ? L_NL : 0);
+      tl = nxt;
+    }
+  }
+}
+
 // Weights [K, N] of one expert to codes and scales. A workgroup takes 128
 // positions of 64 columns: rows of 64 bf16 are read whole, transposed through
 // LDS, and 16 codes of a column leave as one 16-byte piece.
@@ -262,6 +636,21 @@ hipError_t launch_small(const void* A, const void* As, const int32_t* perm, int6
 hipError_t launch_gemm_fp8(const void* A, const void* As, const int32_t* perm, int64_t a_rows, const int32_t* offsets,
                            const void* B, const void* Bs, void* C, void* Cs, int64_t R, int K, int N, int E, bool act,
                            hipStream_t s) {
+  if (R > 40 * (int64_t)E) {
+    const int n_tiles = (int)ceil_div(N, L_BN);
+    const int64_t tiles = m_tiles_bound(R, E, L_BM) * n_tiles;
+    if (tiles > INT32_MAX) return hipErrorInvalidValue;
+    const unsigned grid = (unsigned)max((int64_t)8, min(ceil_div(tiles, 8) * 8, (int64_t)device_cus() / 8 * 8));
+#define MOE_LAUNCH(ACT_, GATHER_)                                                                                 \
+  hipLaunchKernelGGL((gemm_fp8_kernel<ACT_, GATHER_>), dim3(grid), dim3(L_NW * kWave), 0, s, (const uint8_t*)A,     \
+                     (const uint8_t*)As, perm, a_rows, offsets, (const uint8_t*)B, (const uint8_t*)Bs, C,         \
+                     (uint8_t*)Cs, R, K, N, E, n_tiles, group_m())
+    if (act && perm) MOE_LAUNCH(true, true);
+    else if (act) MOE_LAUNCH(true, false);
+    else MOE_LAUNCH(false, false);
+#undef MOE_LAUNCH
+    return hipGetLastError();
+  }
   if (act) return launch_small<1, 4, 4, true>(A, As, perm, a_rows, offsets, B, Bs, C, Cs, R, K, N, E, s);
   return launch_small<1, 2, 4, false>(A, As, perm, a_rows, offsets, B, Bs, C, Cs, R, K, N, E, s);
 }
