@@ -139,7 +139,7 @@ moe_status_t moex_quantize_experts(const moe_problem_t* p, const void* W1, const
  *   rows of y_perm outside [0, offsets[E]) are left untouched
  *   ws at least moex_workspace_size(p, MOEX_STAGE_FFN_FP8) bytes
  * bf16 problems only; MOE_ERR_UNSUPPORTED also when the codes of x8, or those of
- * one expert's weight, reach 2 GiB. */
+ * one expert's weight, reach 2 GiB, or a width 2^22. */
 moe_status_t moex_grouped_ffn_fp8(const moe_problem_t* p, const void* x8, const void* x_scale, const int32_t* perm,
                                   const int32_t* offsets, const void* W1q, const void* W1s, const void* W2q,
                                   const void* W2s, void* y_perm, void* ws, size_t ws_bytes, void* stream);

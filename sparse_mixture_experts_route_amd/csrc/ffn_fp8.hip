@@ -215,44 +215,105 @@ __global__ __launch_bounds__(NG * KS * kWave) void gemm_fp8_small_kernel(
 //
 // Eight waves of 64 x 128 (two per SIMD: one multiplies while the other issues
 // loads), a step of 128 positions, two LDS stages of 64 KB filled by direct
-// loads, persistent workgroups over the tile list of tiles.h. A sits
+// loads, persistent workgroups over a tile list made on the device. A sits
 // row-major in LDS with the 16-byte piece index XOR-ed by (row >> 1) & 7, so
 // the 16 lanes served together touch every bank once; a stage of B is a
 // straight copy of the weight layout, in which a wave's fragment read is 1 KB
-// in lane order. The scales of 16 steps, 16 bytes a row, are one load per wave
+// in lane order. The scales of four steps, a dword a row, are one load per wave
 // and come in two windows used in turn. A fragment of B is read again as soon
 // as the two instructions that use it are issued, so only A needs two register
 // sets: 192 of the 256 registers that two waves per SIMD leave hold operands
 // and sums.
+//
+// The ring runs on across tiles: a tile's last two steps already load the next
+// tile's first two stages, and the epilogue works in 2 KB of LDS per wave of
+// its own while they arrive. Tiles are short (8 to 64 steps), so a ring that
+// drained between them cost a third of the time.
 constexpr int L_BM = 256, L_BN = 256, L_NW = 8, L_WN = 2, L_TM = 2, L_TN = 4;
 constexpr int L_A = L_BM * kQBlock, L_B = L_BN * kQBlock, L_STAGE = L_A + L_B;
-constexpr int L_WIN = 8192;       // 16 steps' scales of 256 rows and 256 columns
+constexpr int L_WIN = 2048;       // four steps' scales of 256 rows, then of 256 columns
+constexpr int L_EP = 2048;        // epilogue staging per wave
 constexpr int L_NL = L_STAGE / 1024 / L_NW;  // loads per wave and stage
 constexpr int L_ALD = L_NL / 2;
+
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// 4 bytes per lane into LDS when `now` is 0 (wave-uniform). The branch stays
+// inside the block: in the source it would end the basic block, and the matrix
+// instructions before it would sink behind it.
+__device__ __forceinline__ void buffer_load_lds4_if0(int now, i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
+  asm volatile(
+      "s_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 .Lmoe_win%=\n\ts_mov_b32 m0, %1\n\t"
+      "buffer_load_dword %2, %3, %4 offen lds\n.Lmoe_win%=:"
+      :
+      : "s"(now), "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
+      : "memory", "m0", "scc");
+}
+#pragma clang diagnostic pop
+
+// At most N of this wave's vector-memory operations outstanding, none when `all` is 0 (wave-uniform).
+template <int N>
+__device__ __forceinline__ void wait_vmem_all_if0(int all) {
+  asm volatile(
+      "s_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 .Lmoe_wait%=\n\ts_waitcnt vmcnt(0)\n.Lmoe_wait%=:\n\ts_waitcnt vmcnt(%1)"
+      :
+      : "s"(all), "n"(N)
+      : "memory", "scc");
+}
 
 template <bool ACT, bool GATHER>
 __global__ __launch_bounds__(L_NW * kWave, 1) void gemm_fp8_kernel(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ As, const int32_t* __restrict__ perm, int64_t a_rows,
     const int32_t* __restrict__ offsets, const uint8_t* __restrict__ B, const uint8_t* __restrict__ Bs,
     void* __restrict__ C, uint8_t* __restrict__ Cs, int64_t R, int K, int N, int E, int n_tiles, int gm) {
-  __shared__ __attribute__((aligned(1024))) char smem[2 * L_STAGE + 2 * L_WIN];
-  __shared__ int s_tstart[257];
-  __shared__ int s_mtiles[256];
+  __shared__ __attribute__((aligned(1024))) char smem[2 * L_STAGE + 2 * L_WIN + L_NW * L_EP];
+  __shared__ int s_tstart[257];  // first tile of each expert, and their number
+  __shared__ int s_lo[256], s_hi[256];  // its rows
   const int tid = threadIdx.x, lane = tid % kWave, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  build_tile_list<L_BM>(offsets, E, R, n_tiles, s_tstart, s_mtiles);
-  const int total = s_tstart[E];
+  if (wave == 0) {
+    int lo4[4], hi4[4], cnt[4], local = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = lane * 4 + i;
+      lo4[i] = hi4[i] = 0;
+      if (e < E) {
+        lo4[i] = max(offsets[e], 0);
+        hi4[i] = (int)min((int64_t)offsets[e + 1], R);
+        s_lo[e] = lo4[i];
+        s_hi[e] = hi4[i];
+      }
+      cnt[i] = hi4[i] > lo4[i] ? (int)ceil_div(hi4[i] - lo4[i], L_BM) * n_tiles : 0;
+      local += cnt[i];
+    }
+    int incl = local;
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+      const int v = __shfl_up(incl, o, kWave);
+      if (lane >= o) incl += v;
+    }
+    int run = incl - local;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (lane * 4 + i < E) s_tstart[lane * 4 + i] = run;
+      run += cnt[i];
+    }
+    if (lane == kWave - 1) s_tstart[E] = incl;
+  }
+  __syncthreads();
+  const int total = __builtin_amdgcn_readfirstlane(s_tstart[E]);
+  // a contiguous share of the tile list per XCD (workgroups are dealt to the 8 XCDs in turn)
   const int xcd = blockIdx.x % 8, nb = gridDim.x / 8, j = blockIdx.x / 8;
   const int lo = (int)((int64_t)total * xcd / 8), hi = (int)((int64_t)total * (xcd + 1) / 8);
   const int n_items = hi - lo > j ? (hi - lo - j - 1) / nb + 1 : 0;
-  const int cp = (int)code_pitch(K), sp = (int)scale_pitch(K), KB = cp / kQBlock;
+  if (n_items == 0) return;
+  const int cp = (int)code_pitch(K), sp = (int)scale_pitch(K), KB = cp / kQBlock;  // KB >= 2
   lds_char* const lds = (lds_char*)smem;
   const uint32_t lds_base = lds_addr(smem);
   const int wm0 = (wave / L_WN) * (L_TM * 32), wn0 = (wave % L_WN) * (L_TN * 32);
 
   struct Tile {
-    int e, n0;
-    int64_t row0, row_end;
+    int e, n0, row0, rows;  // rows of the group from row0 on, at most L_BM
   };
   struct Loads {
     i32x4 rsA, rsB, rsS;
@@ -267,39 +328,45 @@ __global__ __launch_bounds__(L_NW * kWave, 1) void gemm_fp8_kernel(
     a_c16[i] = pc.c * 16;
   }
   const int s_row = (wave & 3) * 64 + lane;
-  auto locate = [&](int t) {
-    int a0 = 0, a1 = E;
-    while (a1 - a0 > 1) {
-      const int mid = (a0 + a1) >> 1;
-      if (s_tstart[mid] <= t) a0 = mid; else a1 = mid;
+  // tile t; past the workgroup's last item: no rows and no columns
+  auto locate = [&](int item) {
+    Tile tl = {0, 0, 0, 0};
+    if (item >= n_items) return tl;
+    const int t = lo + j + item * nb;
+    int e = 0;  // experts after the first that start at or before t
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int q = 1 + i * kWave + lane;
+      e += __popcll(__ballot(q < E && s_tstart[q < E ? q : 0] <= t));
     }
-    Tile tl;
-    tl.e = __builtin_amdgcn_readfirstlane(a0);
-    const int local = t - __builtin_amdgcn_readfirstlane(s_tstart[tl.e]);
-    const int mt = __builtin_amdgcn_readfirstlane(s_mtiles[tl.e]);
+    tl.e = __builtin_amdgcn_readfirstlane(e);
+    const int first = __builtin_amdgcn_readfirstlane(s_lo[tl.e]), end = __builtin_amdgcn_readfirstlane(s_hi[tl.e]);
+    const int mt = (int)ceil_div(end - first, L_BM);
     int n_tile, m_idx;
-    tile_coords(local, mt, n_tiles, gm, n_tile, m_idx);
-    tl.row0 = (int64_t)max(__builtin_amdgcn_readfirstlane(offsets[tl.e]), 0) + (int64_t)m_idx * L_BM;
-    tl.row_end = min((int64_t)__builtin_amdgcn_readfirstlane(offsets[tl.e + 1]), R);
+    tile_coords(t - __builtin_amdgcn_readfirstlane(s_tstart[tl.e]), mt, n_tiles, gm, n_tile, m_idx);
+    tl.row0 = first + m_idx * L_BM;
+    tl.rows = min(end - tl.row0, L_BM);
     tl.n0 = n_tile * L_BN;
     return tl;
   };
   auto load_perm = [&](const Tile& t_, int (&pv)[L_ALD + 1]) {
 #pragma unroll
     for (int i = 0; i <= L_ALD; ++i) {
-      const int64_t r = t_.row0 + (i < L_ALD ? a_row[i < L_ALD ? i : 0] : s_row);
-      pv[i] = r < t_.row_end ? perm[r] : -1;
+      const int r = i < L_ALD ? a_row[i < L_ALD ? i : 0] : s_row;
+      pv[i] = r < t_.rows ? perm[t_.row0 + r] : -1;
     }
   };
   auto bind = [&](const Tile& t_, const int (&pv)[L_ALD + 1]) {
     Loads l;
-    const int rows = (int)min(t_.row_end - t_.row0, (int64_t)L_BM);
-    l.rsA = GATHER ? buffer_rsrc(A, (uint32_t)(a_rows * cp)) : buffer_rsrc(A + t_.row0 * cp, (uint32_t)(rows * cp));
-    l.rsB = buffer_rsrc(B + (int64_t)t_.e * N * cp, (uint32_t)((int64_t)N * cp));
+    const bool some = t_.rows > 0;
+    l.rsA = GATHER ? buffer_rsrc(A, some ? (uint32_t)(a_rows * cp) : 0u)
+                   : buffer_rsrc(A + (int64_t)t_.row0 * cp, (uint32_t)(t_.rows * cp));
+    l.rsB = buffer_rsrc(B + (int64_t)t_.e * N * cp, some ? (uint32_t)((int64_t)N * cp) : 0u);
     if (wave < 4)
-      l.rsS = GATHER ? buffer_rsrc(As, (uint32_t)(a_rows * sp)) : buffer_rsrc(As + t_.row0 * sp, (uint32_t)(rows * sp));
+      l.rsS = GATHER ? buffer_rsrc(As, some ? (uint32_t)(a_rows * sp) : 0u)
+                     : buffer_rsrc(As + (int64_t)t_.row0 * sp, (uint32_t)(t_.rows * sp));
     else
-      l.rsS = buffer_rsrc(Bs + (int64_t)t_.e * N * KB, (uint32_t)((int64_t)N * KB));
+      l.rsS = buffer_rsrc(Bs + (int64_t)t_.e * N * KB, some ? (uint32_t)((int64_t)N * KB) : 0u);
 #pragma unroll
     for (int i = 0; i <= L_ALD; ++i) {
       const int row = i < L_ALD ? a_row[i < L_ALD ? i : 0] : s_row;
@@ -314,42 +381,42 @@ __global__ __launch_bounds__(L_NW * kWave, 1) void gemm_fp8_kernel(
     l.gb = g * 32 < N ? (uint32_t)g * (uint32_t)(KB * 4096) + lane * 16 : lanes::kOutOfRange;
     if (wave >= 4) {
       const int sg = t_.n0 / 32 + (wave - 4) * 2 + half;
-      l.gs = sg * 32 < N ? (uint32_t)sg * (uint32_t)(KB * 32) + (lane & 31) * 16 : lanes::kOutOfRange;
+      l.gs = sg * 32 < N ? (uint32_t)sg * (uint32_t)(KB * 32) + (lane & 31) * 4 : lanes::kOutOfRange;
     }
     return l;
   };
-  // the scales of steps 16 w .. 16 w + 15
-  auto issue_window = [&](const Loads& l, int w) {
-    buffer_load_lds16(l.rsS, l.gs, (uint32_t)w * (wave < 4 ? 16u : 512u),
-                      lds_base + 2 * L_STAGE + (w & 1) * L_WIN + wave * 1024);
-  };
-  // load `i` of step kt's stage into ring buffer kt & 1
-  auto issue_one = [&](const Loads& l, int kt, int i) {
+  // Load `i` of step kt's stage into ring buffer `buf`. Windows: that of steps
+  // 4 w .. goes out before the first of them, into the buffer of window w - 2,
+  // whose last scales were read two steps ago.
+  auto issue_one = [&](const Loads& l, int kt, int buf, int i) {
     if (i < L_ALD)
-      buffer_load_lds16(l.rsA, l.ga[i], (uint32_t)kt * kQBlock,
-                        lds_base + (kt & 1) * L_A + (wave * L_ALD + i) * 1024);
+      buffer_load_lds16(l.rsA, l.ga[i], (uint32_t)kt * kQBlock, lds_base + buf * L_A + (wave * L_ALD + i) * 1024);
     else
       buffer_load_lds16(l.rsB, l.gb, (uint32_t)kt * 4096u + (i - L_ALD) * 1024u,
-                        lds_base + 2 * L_A + (kt & 1) * L_B + wave * 4096 + (i - L_ALD) * 1024);
+                        lds_base + 2 * L_A + buf * L_B + wave * 4096 + (i - L_ALD) * 1024);
+  };
+  auto issue_window = [&](const Loads& l, int kt, int wbuf) {
+    buffer_load_lds4_if0(kt & 3, l.rsS, l.gs, (uint32_t)(kt >> 2) * (wave < 4 ? 4u : 128u),
+                         lds_base + 2 * L_STAGE + wbuf * L_WIN + wave * 256);
   };
 
   i32x8 fa[2][L_TM], fb[L_TN];
   int sa = 0, sb = 0, sa_n[L_TM], sb_n[L_TN];  // the scale bytes of a step, one per byte
   f32x16 acc[L_TM][L_TN];
   typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+  typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
+  typedef __attribute__((address_space(3))) uint32_t lds_u32;
   typedef __attribute__((address_space(3))) uint8_t lds_u8;
   // LDS addresses of this lane's fragment pieces in the buffer being read: both
   // operands' buffers are L_A apart, so a step moves them all by +-L_A
   static_assert(L_A == L_B, "one distance moves both operands' addresses");
   uint32_t ra[4], rb;
-  auto first_addresses = [&]() {
-    const int sw = ((lane & 31) >> 1) & 7;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) ra[q] = lds_base + (wm0 + (lane & 31)) * kQBlock + (((2 * q + half) ^ sw) << 4);
-    rb = lds_base + 2 * L_A + wn0 * kQBlock + lane * 16;
-  };
-  auto move_addresses = [&](int kt) {  // to the buffer of step kt
-    const uint32_t d = (kt & 1) ? (uint32_t)L_A : (uint32_t)-L_A;
+  for (int q = 0; q < 4; ++q)
+    ra[q] = lds_base + (wm0 + (lane & 31)) * kQBlock + (((2 * q + half) ^ (((lane & 31) >> 1) & 7)) << 4);
+  rb = lds_base + 2 * L_A + wn0 * kQBlock + lane * 16;
+  auto move_addresses = [&](int buf) {  // to ring buffer `buf` from the other one
+    const uint32_t d = buf ? (uint32_t)L_A : (uint32_t)-L_A;
 #pragma unroll
     for (int q = 0; q < 4; ++q) asm("v_add_u32 %0, %0, %1" : "+v"(ra[q]) : "s"(d));
     asm("v_add_u32 %0, %0, %1" : "+v"(rb) : "s"(d));
@@ -362,13 +429,13 @@ __global__ __launch_bounds__(L_NW * kWave, 1) void gemm_fp8_kernel(
     fb[ni] = join8(*(lds_u32x4*)(uintptr_t)(rb + ni * 4096 + js * 2048),
                    *(lds_u32x4*)(uintptr_t)(rb + ni * 4096 + js * 2048 + 1024));
   };
-  auto read_scales = [&](int kt) {
-    lds_char* w = lds + 2 * L_STAGE + ((kt >> 4) & 1) * L_WIN + (kt & 15);
+  auto read_scales = [&](int kt, int wbuf) {
+    lds_char* const w = lds + 2 * L_STAGE + wbuf * L_WIN;
 #pragma unroll
-    for (int mi = 0; mi < L_TM; ++mi) sa_n[mi] = *(lds_u8*)(w + (wm0 + (lane & 31)) * 16 + mi * 512);
-    w += 31 * (kt & 15);
+    for (int mi = 0; mi < L_TM; ++mi) sa_n[mi] = *(lds_u8*)(w + (kt & 3) + (wm0 + (lane & 31)) * 4 + mi * 128);
 #pragma unroll
-    for (int ni = 0; ni < L_TN; ++ni) sb_n[ni] = *(lds_u8*)(w + 4096 + wn0 * 16 + (lane & 31) + ni * 512);
+    for (int ni = 0; ni < L_TN; ++ni)
+      sb_n[ni] = *(lds_u8*)(w + 1024 + (kt & 3) * 32 + wn0 * 4 + (lane & 31) + ni * 128);
   };
   auto take_scales = [&]() {
     sa = sa_n[0] | sa_n[1] << 8;
@@ -392,11 +459,16 @@ __global__ __launch_bounds__(L_NW * kWave, 1) void gemm_fp8_kernel(
     else if (ni == 2) two(IntC<2>{});
     else two(IntC<3>{});
   };
-  // One step of 128 positions. MORE: another step follows (its stage has to have
-  // landed, and its first fragments are read here); REFILL: step kt + 2 is
-  // loaded into the buffer that this step leaves.
-  auto step = [&](const Loads& l, int kt, auto more_c, auto refill_c) {
-    constexpr bool MORE = decltype(more_c)::value, REFILL = decltype(refill_c)::value;
+  // stores of an epilogue, each issued whatever its lanes hold
+  constexpr int EP_ST = ACT ? 8 + L_TM : 16;
+  // One step of 128 positions from ring buffer `buf`. After the barrier in its
+  // middle that buffer is free: step `fill` of `l` is loaded into it, its window
+  // (when it starts one) into `fwin`. LAST (of a tile): the next step's stage is
+  // waited for after the epilogue. Else the next step kt + 1 has to have landed
+  // (its scales in window `nwin`) and its first fragments are read here; `stores`
+  // is not 0 where an epilogue's stores came after the loads waited for.
+  auto step = [&](const Loads& l, int kt, int buf, int nwin, int fill, int fwin, int stores, auto last_c) {
+    constexpr bool LAST = decltype(last_c)::value;
 #pragma unroll
     for (int ni = 0; ni < L_TN; ++ni)
       mfma_pair(0, ni, [&](int mi) {
@@ -405,112 +477,96 @@ __global__ __launch_bounds__(L_NW * kWave, 1) void gemm_fp8_kernel(
       });
 #pragma unroll
     for (int ni = 0; ni < L_TN / 2; ++ni) mfma_pair(1, ni, [](int) {});
-    if constexpr (MORE) {
-      wait_vmem<0>();   // step kt + 1 has landed
-      __syncthreads();  // for every wave, and every wave is done reading this buffer
-      move_addresses(kt + 1);
-      read_scales(kt + 1);
+    if constexpr (!LAST) wait_vmem_all_if0<EP_ST>(stores);
+    __syncthreads();  // step kt + 1 is in for every wave, and every wave is done reading this buffer
+    if constexpr (!LAST) {
+      move_addresses(buf ^ 1);
+      read_scales(kt + 1, nwin);
 #pragma unroll
       for (int mi = 0; mi < L_TM; ++mi) read_a(0, mi);
 #pragma unroll
       for (int ni = 0; ni < L_TN / 2; ++ni) read_b(0, ni);
     }
+    issue_window(l, fill, fwin);
 #pragma unroll
     for (int ni = L_TN / 2; ni < L_TN; ++ni)
       mfma_pair(1, ni, [&](int mi) {
-        if (MORE && mi == 1) read_b(0, ni);
-        if constexpr (REFILL) {
-          const int at = (ni - L_TN / 2) * L_TM + mi;  // 0 .. 3: two loads each
-          issue_one(l, kt + 2, 2 * at);
-          issue_one(l, kt + 2, 2 * at + 1);
-        }
+        if (!LAST && mi == 1) read_b(0, ni);
+        const int at = (ni - L_TN / 2) * L_TM + mi;  // 0 .. 3: two loads each
+        issue_one(l, fill, buf, 2 * at);
+        issue_one(l, fill, buf, 2 * at + 1);
       });
-    if constexpr (MORE) take_scales();
+    if constexpr (!LAST) take_scales();
+  };
+  auto idle_step = [&](const Loads& l, int buf, int fill, int fwin, int stores, bool last) {
+    if (!last) wait_vmem_all_if0<EP_ST>(stores);
+    __syncthreads();
+    issue_window(l, fill, fwin);
+#pragma unroll
+    for (int i = 0; i < L_NL; ++i) issue_one(l, fill, buf, i);
   };
 
-  Tile tl;
+  Tile tl = locate(0), nxt;
   Loads ld;
-  if (n_items > 0) {
-    tl = locate(lo + j);
-    int pv[L_ALD + 1];
-    if constexpr (GATHER) load_perm(tl, pv);
-    ld = bind(tl, pv);
-    issue_window(ld, 0);
+  int npv[L_ALD + 1];
+  if constexpr (GATHER) load_perm(tl, npv);
+  ld = bind(tl, npv);
+  issue_window(ld, 0, 0);
 #pragma unroll
-    for (int i = 0; i < L_NL; ++i) issue_one(ld, 0, i);
-    if (KB > 1)
+  for (int s2 = 0; s2 < 2; ++s2)
 #pragma unroll
-      for (int i = 0; i < L_NL; ++i) issue_one(ld, 1, i);
-  }
-  // memory operations issued after an item's stage 0 (each is issued whatever its lanes hold)
-  constexpr int EP_ST = ACT ? 8 + L_TM : 16;
-  int pend = KB > 1 ? L_NL : 0;
+    for (int i = 0; i < L_NL; ++i) issue_one(ld, s2, s2, i);
+  int buf = 0, win = 0;  // ring buffer and window of the tile's first step
+  const int nwins = (KB + 3) >> 2;
 
   for (int item = 0; item < n_items; ++item) {
-    if (pend == 0) wait_vmem<0>();
-    else if (pend == L_NL) wait_vmem<L_NL>();
-    else if (pend == EP_ST) wait_vmem<EP_ST>();
-    else wait_vmem<EP_ST + L_NL>();
+    // the tile's first stage: its second one, and the last tile's stores, were issued after it
+    if (item == 0) wait_vmem<L_NL>();
+    else wait_vmem<L_NL + EP_ST>();
     __syncthreads();
-    const bool has_next = item + 1 < n_items;
-    Tile nxt = tl;
-    int npv[L_ALD + 1];
-    if (has_next) {
-      nxt = locate(lo + j + (item + 1) * nb);
-      if constexpr (GATHER) load_perm(nxt, npv);
-    }
+    nxt = locate(item + 1);
+    if constexpr (GATHER) load_perm(nxt, npv);
 #pragma unroll
     for (int mi = 0; mi < L_TM; ++mi)
 #pragma unroll
       for (int ni = 0; ni < L_TN; ++ni)
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[mi][ni][v] = 0.0f;
-    if (tl.row_end - tl.row0 > wm0) {
-      read_scales(0);
+    // window of step kt: win + kt / 4; of the next tile's first steps: win + nwins
+    if (tl.rows > wm0) {
+      read_scales(0, win & 1);
       take_scales();
-      first_addresses();
 #pragma unroll
       for (int mi = 0; mi < L_TM; ++mi) read_a(0, mi);
 #pragma unroll
       for (int ni = 0; ni < L_TN; ++ni) read_b(0, ni);
-      for (int w = 0; 16 * w < KB - 2; ++w) {
-        // the next window goes out with this one's first step: the window before this one is read no more
-        if (16 * (w + 1) < KB) issue_window(ld, w + 1);
-        for (int kt = 16 * w; kt < min(16 * (w + 1), KB - 2); ++kt) step(ld, kt, BoolC<true>{}, BoolC<true>{});
-      }
-      if (KB > 1) step(ld, KB - 2, BoolC<true>{}, BoolC<false>{});
-      step(ld, KB - 1, BoolC<false>{}, BoolC<false>{});
-    } else {
-      // all of this wave's rows lie past the group's end: only its share of the loads
-      for (int kt = 0; kt < KB - 1; ++kt) {
-        if ((kt & 15) == 0 && kt + 16 < KB) issue_window(ld, (kt >> 4) + 1);
-        wait_vmem<0>();
-        __syncthreads();
-        if (kt + 2 < KB) {
-#pragma unroll
-          for (int i = 0; i < L_NL; ++i) issue_one(ld, kt + 2, i);
-        }
-      }
-    }
-    __syncthreads();  // every wave is done with every buffer
-
-    // the next item's first stage goes out before this item's epilogue, which works in buffer 1
-    if (has_next) {
+      for (int kt = 0; kt < KB - 2; ++kt)
+        step(ld, kt, (buf + kt) & 1, (win + ((kt + 1) >> 2)) & 1, kt + 2, (win + ((kt + 2) >> 2)) & 1,
+             kt == 0 ? item : 0, BoolC<false>{});
       ld = bind(nxt, npv);
-      issue_window(ld, 0);
-#pragma unroll
-      for (int i = 0; i < L_NL; ++i) issue_one(ld, 0, i);
+      step(ld, KB - 2, (buf + KB) & 1, (win + ((KB - 1) >> 2)) & 1, 0, (win + nwins) & 1, KB == 2 ? item : 0,
+           BoolC<false>{});
+      step(ld, KB - 1, (buf + KB + 1) & 1, 0, 1, 0, 0, BoolC<true>{});
+      move_addresses((buf + KB) & 1);
+    } else {
+      // all of this wave's rows lie past the group's end: its share of the loads alone
+      for (int kt = 0; kt < KB - 2; ++kt)
+        idle_step(ld, (buf + kt) & 1, kt + 2, (win + ((kt + 2) >> 2)) & 1, kt == 0 ? item : 0, false);
+      ld = bind(nxt, npv);
+      idle_step(ld, (buf + KB) & 1, 0, (win + nwins) & 1, KB == 2 ? item : 0, false);
+      idle_step(ld, (buf + KB + 1) & 1, 1, 0, 0, true);
+      if (KB & 1) move_addresses((buf + 1) & 1);
     }
-    lds_char* const ep = lds + (wave < 4 ? L_A : 2 * L_A + L_B - 4 * 8192) + wave * 8192;  // buffer 1 of A, then of B
-    typedef __attribute__((address_space(3))) uint32_t lds_u32;
-    typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
-    const int rows = (int)min(tl.row_end - tl.row0, (int64_t)L_BM);
+
+    lds_char* const ep = lds + 2 * L_STAGE + 2 * L_WIN + wave * L_EP;
+    // 32 rows of 64 bytes at a time: pieces of 16 bytes, XOR-ed by the row
+    auto ep_at = [&](int row, int ch) { return ep + row * 64 + ((ch ^ ((row >> 2) & 3)) << 4); };
     if constexpr (ACT) {
       const int hp = (int)code_pitch(N), hs = (int)scale_pitch(N);
       const __amdgpu_buffer_rsrc_t rsC = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)((uint8_t*)C + tl.row0 * hp), (short)0, rows * hp, kBufferFlags);
-      const __amdgpu_buffer_rsrc_t rsCs =
-          __builtin_amdgcn_make_buffer_rsrc((void*)(Cs + tl.row0 * hs), (short)0, rows * hs, kBufferFlags);
+          (void*)((uint8_t*)C + (int64_t)tl.row0 * hp), (short)0, tl.rows * hp, kBufferFlags);
+      const __amdgpu_buffer_rsrc_t rsCs = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(Cs + (int64_t)tl.row0 * hs), (short)0, tl.rows * hs, kBufferFlags);
       const int col = tl.n0 + wn0;
       const bool cols = col < hp;
 #pragma unroll
@@ -526,60 +582,58 @@ __global__ __launch_bounds__(L_NW * kWave, 1) void gemm_fp8_kernel(
         m = fmaxf(m, __shfl_xor(m, 32, kWave));
         const int byte = scale_byte(m);
         const float inv = inv_scale(byte);
-        const int row = mi * 32 + (lane & 31);
+        const int row = lane & 31;
 #pragma unroll
-        for (int ni = 0; ni < L_TN; ++ni)
+        for (int np = 0; np < 2; ++np) {  // 64 columns at a time
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const int ch = ni * 2 + (v >> 1);
-            *(lds_u32*)(ep + row * 128 + ((ch ^ (row & 7)) << 4) + (v & 1) * 8 + half * 4) =
-                encode4(acc[mi][ni][4 * v], acc[mi][ni][4 * v + 1], acc[mi][ni][4 * v + 2], acc[mi][ni][4 * v + 3], inv);
+          for (int v = 0; v < 8; ++v) {
+            const int ni = np * 2 + v / 4, q = v % 4;
+            *(lds_u32*)(ep_at(row, v / 2) + (v & 1) * 8 + half * 4) =
+                encode4(acc[mi][ni][4 * q], acc[mi][ni][4 * q + 1], acc[mi][ni][4 * q + 2], acc[mi][ni][4 * q + 3], inv);
           }
-        __builtin_amdgcn_raw_buffer_store_b8((uint8_t)byte, rsCs,
-                                             cols && half == 0 ? (wm0 + row) * hs + col / kQBlock : 0x7FFFFFF0, 0, 0);
-        __builtin_amdgcn_sched_barrier(0);
-      }
+          // a wave's LDS operations complete in order: no barrier before its own reads
 #pragma unroll
-      for (int it = 0; it < 8; ++it) {
-        const int row = it * 8 + lane / 8, ch = lane % 8;
-        const u32x4 v = *(lds_u32x4*)(ep + row * 128 + ((ch ^ (row & 7)) << 4));
-        __builtin_amdgcn_raw_buffer_store_b128(v, rsC, cols ? (wm0 + row) * hp + col + ch * 16 : 0x7FFFFFF0, 0, 0);
+          for (int it = 0; it < 2; ++it) {
+            const int r = it * 16 + lane / 4, ch = lane % 4;
+            const u32x4 v = *(lds_u32x4*)ep_at(r, ch);
+            __builtin_amdgcn_raw_buffer_store_b128(
+                v, rsC, cols ? (wm0 + mi * 32 + r) * hp + col + np * 64 + ch * 16 : 0x7FFFFFF0, 0, 0);
+          }
+        }
+        __builtin_amdgcn_raw_buffer_store_b8((uint8_t)byte, rsCs,
+                                             cols && half == 0 ? (wm0 + mi * 32 + row) * hs + col / kQBlock : 0x7FFFFFF0,
+                                             0, 0);
+        __builtin_amdgcn_sched_barrier(0);
       }
     } else {
       const __amdgpu_buffer_rsrc_t rsC = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)((bf16_bits*)C + tl.row0 * N), (short)0, rows * N * 2, kBufferFlags);
+          (void*)((bf16_bits*)C + (int64_t)tl.row0 * N), (short)0, tl.rows * N * 2, kBufferFlags);
 #pragma unroll
-      for (int mi = 0; mi < L_TM; ++mi) {
+      for (int mi = 0; mi < L_TM; ++mi)
 #pragma unroll
-        for (int ni = 0; ni < L_TN; ++ni)
+        for (int ni = 0; ni < L_TN; ++ni) {
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             u32x2 o;
             o[0] = pack_bf16x2(acc[mi][ni][4 * v], acc[mi][ni][4 * v + 1]);
             o[1] = pack_bf16x2(acc[mi][ni][4 * v + 2], acc[mi][ni][4 * v + 3]);
-            const int row = lane & 31, ch = ni * 4 + v;  // 32 rows of 256 bytes, 16 pieces
-            *(lds_u32x2*)(ep + row * 256 + ((ch ^ (row & 15)) << 4) + half * 8) = o;
+            *(lds_u32x2*)(ep_at(lane & 31, v) + half * 8) = o;
           }
-        // a wave's LDS operations complete in order: no barrier before its own reads
 #pragma unroll
-        for (int it = 0; it < 8; ++it) {
-          const int row = it * 4 + lane / 16, ch = lane % 16;
-          const u32x4 v = *(lds_u32x4*)(ep + row * 256 + ((ch ^ (row & 15)) << 4));
-          const int n = tl.n0 + wn0 + ch * 8;
-          __builtin_amdgcn_raw_buffer_store_b128(v, rsC, lanes::c_store_off(wm0 + mi * 32 + row, n, N), 0, 0);
+          for (int it = 0; it < 2; ++it) {
+            const int r = it * 16 + lane / 4, ch = lane % 4;
+            const u32x4 v = *(lds_u32x4*)ep_at(r, ch);
+            const int n = tl.n0 + wn0 + ni * 32 + ch * 8;
+            __builtin_amdgcn_raw_buffer_store_b128(v, rsC, lanes::c_store_off(wm0 + mi * 32 + r, n, N), 0, 0);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);
-      }
     }
-    if (has_next) {
-      __syncthreads();  // every wave has read its piece of buffer 1
-      if (KB > 1)
-#pragma unroll
-        for (int i = 0; i < L_NL; ++i) issue_one(ld, 1, i);
-      pend = EP_ST + (KB > 1 ? L_NL : 0);
-      tl = nxt;
-    }
+    tl = nxt;
+    buf = (buf + KB) & 1;
+    win += nwins;
   }
+  wait_vmem<0>();  // the loads past the last tile (of no bytes) have ended before the LDS is given back
 }
 
 // Weights [K, N] of one expert to codes and scales. A workgroup takes 128
@@ -636,7 +690,7 @@ hipError_t launch_small(const void* A, const void* As, const int32_t* perm, int6
 hipError_t launch_gemm_fp8(const void* A, const void* As, const int32_t* perm, int64_t a_rows, const int32_t* offsets,
                            const void* B, const void* Bs, void* C, void* Cs, int64_t R, int K, int N, int E, bool act,
                            hipStream_t s) {
-  if (R > 40 * (int64_t)E) {
+  if (R > 40 * (int64_t)E && K > kQBlock) {
     const int n_tiles = (int)ceil_div(N, L_BN);
     const int64_t tiles = m_tiles_bound(R, E, L_BM) * n_tiles;
     if (tiles > INT32_MAX) return hipErrorInvalidValue;

@@ -42,11 +42,13 @@ bool buffers_ok(std::initializer_list<Buf> bufs) {
   return true;
 }
 
-// Codes of x8 and of one expert's weight are read with 32-bit byte offsets.
+// Codes of x8, of one expert's weight and of a tile's 256 rows (bf16 rows of
+// the result included) are reached with 32-bit byte offsets.
 bool fp8_supported(const moe_problem_t& p, bool gathered) {
   const int64_t rows = gathered ? p.T : p.T * p.k;
-  const int64_t lim = (int64_t)INT32_MAX, cd = (int64_t)moex_code_pitch(p.d_model), ce = (int64_t)moex_code_pitch(p.d_expert);
-  return p.dtype == MOE_DTYPE_BF16 && rows * cd < lim && p.d_expert * cd < lim && p.d_model * ce < lim;
+  const int64_t lim = INT32_MAX, cd = (int64_t)moex_code_pitch(p.d_model), ce = (int64_t)moex_code_pitch(p.d_expert);
+  return p.dtype == MOE_DTYPE_BF16 && rows * cd < lim && p.d_expert * cd < lim && p.d_model * ce < lim &&
+         512 * cd < lim && 512 * ce < lim;
 }
 
 struct FfnWs {
