@@ -64,57 +64,70 @@ def scale_pitch(K: int) -> int:
     return (int(K) + 2047) // 2048 * 16
 
 
-class _Args:
-    """Checks tensors against what a call expects and finds the device they share."""
+def _ptr(name, t, n, dtypes, dev):
+    """Address of a tensor of n values of one of dtypes on GPU dev."""
+    try:
+        if t.get_device() == dev and t.dtype in dtypes and t.numel() == n and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    raise _refusal(name, t, n, dtypes, dev)
 
-    __slots__ = ("where", "device")
 
-    def __init__(self, where: str):
-        self.where = where
-        self.device = None
+def _opt(name, t, n, dtypes, dev):
+    """The same, or NULL for None."""
+    return None if t is None else _ptr(name, t, n, dtypes, dev)
 
-    def __call__(self, name, t, n, dtypes, required=True):
-        if t is None:
-            if required:
-                raise ValueError(f"{self.where}: {name} is required")
-            return None
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{self.where}: {name} must be a torch.Tensor")
-        if not t.is_cuda:
-            raise ValueError(f"{self.where}: {name} must live on the GPU")
-        if t.dtype not in dtypes:
-            raise TypeError(f"{self.where}: {name} has type {t.dtype}, expected {dtypes[0]}")
-        if t.numel() != n:
-            raise ValueError(f"{self.where}: {name} holds {t.numel()} values, expected {n}")
-        if not t.is_contiguous():
-            raise ValueError(f"{self.where}: {name} must be contiguous")
-        if self.device is None:
-            self.device = t.device
-        elif t.device != self.device:
-            raise ValueError(f"{self.where}: {name} is on {t.device}, other arguments on {self.device}")
-        return t.data_ptr()
 
-    def ws(self, t):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{self.where}: ws must be a torch.Tensor")
-        return self("ws", t, t.numel(), (t.dtype,)), t.numel() * t.element_size()
+def _refusal(name, t, n, dtypes, dev):
+    if t is None:
+        return ValueError(f"{name} is required")
+    if not isinstance(t, torch.Tensor):
+        return TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        return ValueError(f"{name} must live on the GPU")
+    if t.dtype not in dtypes:
+        return TypeError(f"{name} has type {t.dtype}, expected {dtypes[0]}")
+    if t.numel() != n:
+        return ValueError(f"{name} holds {t.numel()} values, expected {n}")
+    if not t.is_contiguous():
+        return ValueError(f"{name} must be contiguous")
+    return ValueError(f"{name} is on {t.device}, other arguments on GPU {dev}")
 
-    def call(self, stream, *args):
-        f = getattr(_c, self.where)
-        dev = self.device
-        if stream is None:
-            stream = torch.cuda.current_stream(dev).cuda_stream
-        elif isinstance(stream, torch.cuda.Stream):
-            if stream.device != dev:
-                raise ValueError(f"{self.where}: the stream is on {stream.device}, the tensors on {dev}")
-            stream = stream.cuda_stream
-        if dev.index == torch.cuda.current_device():
-            status = f(*args, int(stream))
-        else:
-            with torch.cuda.device(dev):
-                status = f(*args, int(stream))
-        if status != _lib.MOE_OK:
-            raise _lib.MoEError(status, self.where)
+
+def _device(name, t):
+    """GPU of the first tensor of a call, which all others have to share."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise _refusal(name, t, 0, (), -1)
+    return t.get_device()
+
+
+def _ws(ws, dev):
+    if not isinstance(ws, torch.Tensor):
+        raise _refusal("ws", ws, 0, (), dev)
+    return _ptr("ws", ws, ws.numel(), (ws.dtype,), dev), ws.numel() * ws.element_size()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call(f, dev, stream, *args):
+    """Calls f on GPU dev and on `stream` (None: that GPU's current stream)."""
+    if stream is None:
+        stream = _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
+    elif isinstance(stream, torch.cuda.Stream):
+        if stream.device.index != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on GPU {dev}")
+        stream = stream.cuda_stream
+    else:
+        stream = int(stream)
+    if dev == torch.cuda.current_device():
+        status = f(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args, stream)
+    if status != _lib.MOE_OK:
+        raise _lib.MoEError(status, f.__name__)
 
 
 def _rows(p: Problem):
@@ -130,48 +143,48 @@ def moex_workspace_size(p: Problem, stage: int) -> int:
 
 
 def moex_add_rmsnorm(p: Problem, x, residual, gain, eps, h, y, y8, y_scale, rstd, stream=None):
-    a, n, dt = _Args("moex_add_rmsnorm"), p.T * p.d_model, _rows(p)
-    args = (ctypes.byref(p), a("x", x, n, dt), a("residual", residual, n, dt, False), a("gain", gain, p.d_model, dt),
-            float(eps), a("h", h, n, dt, False), a("y", y, n, dt, False),
-            a("y8", y8, p.T * code_pitch(p.d_model), _CODE, False),
-            a("y_scale", y_scale, p.T * scale_pitch(p.d_model), _SCALE, False), a("rstd", rstd, p.T, _F32, False))
-    a.call(stream, *args)
+    dev, T, d, dt = _device("x", x), p.T, p.d_model, _rows(p)
+    n = T * d
+    _call(_c.moex_add_rmsnorm, dev, stream, ctypes.byref(p), _ptr("x", x, n, dt, dev),
+          _opt("residual", residual, n, dt, dev), _ptr("gain", gain, d, dt, dev), eps, _opt("h", h, n, dt, dev),
+          _opt("y", y, n, dt, dev), _opt("y8", y8, T * code_pitch(d), _CODE, dev),
+          _opt("y_scale", y_scale, T * scale_pitch(d), _SCALE, dev), _opt("rstd", rstd, T, _F32, dev))
 
 
 def moex_add_rmsnorm_backward(p: Problem, h, gain, rstd, dy, dh, dx, dgain, ws, stream=None):
-    a, n, dt = _Args("moex_add_rmsnorm_backward"), p.T * p.d_model, _rows(p)
-    args = (ctypes.byref(p), a("h", h, n, dt), a("gain", gain, p.d_model, dt), a("rstd", rstd, p.T, _F32),
-            a("dy", dy, n, dt), a("dh", dh, n, dt, False), a("dx", dx, n, dt), a("dgain", dgain, p.d_model, _F32))
-    a.call(stream, *args, *a.ws(ws))
+    dev, T, d, dt = _device("h", h), p.T, p.d_model, _rows(p)
+    n = T * d
+    _call(_c.moex_add_rmsnorm_backward, dev, stream, ctypes.byref(p), _ptr("h", h, n, dt, dev),
+          _ptr("gain", gain, d, dt, dev), _ptr("rstd", rstd, T, _F32, dev), _ptr("dy", dy, n, dt, dev),
+          _opt("dh", dh, n, dt, dev), _ptr("dx", dx, n, dt, dev), _ptr("dgain", dgain, d, _F32, dev), *_ws(ws, dev))
 
 
 def moex_quantize_rows(p: Problem, x, x8, x_scale, stream=None):
-    a = _Args("moex_quantize_rows")
-    args = (ctypes.byref(p), a("x", x, p.T * p.d_model, _rows(p)), a("x8", x8, p.T * code_pitch(p.d_model), _CODE),
-            a("x_scale", x_scale, p.T * scale_pitch(p.d_model), _SCALE))
-    a.call(stream, *args)
+    dev, T, d = _device("x", x), p.T, p.d_model
+    _call(_c.moex_quantize_rows, dev, stream, ctypes.byref(p), _ptr("x", x, T * d, _rows(p), dev),
+          _ptr("x8", x8, T * code_pitch(d), _CODE, dev), _ptr("x_scale", x_scale, T * scale_pitch(d), _SCALE, dev))
 
 
 def moex_balance_loss(p: Problem, logits, topk_idx, token_mask, coef, loss, counts, mean_prob, dlogits, ws,
                       stream=None):
-    a = _Args("moex_balance_loss")
-    args = (ctypes.byref(p), a("logits", logits, p.T * p.E, _F32), a("topk_idx", topk_idx, p.T * p.k, _I32),
-            a("token_mask", token_mask, p.T, _BYTE, False), float(coef), a("loss", loss, 1, _F32),
-            a("counts", counts, p.E, _I32), a("mean_prob", mean_prob, p.E, _F32),
-            a("dlogits", dlogits, p.T * p.E, _F32, False))
-    a.call(stream, *args, *a.ws(ws))
+    dev, T, E = _device("logits", logits), p.T, p.E
+    _call(_c.moex_balance_loss, dev, stream, ctypes.byref(p), _ptr("logits", logits, T * E, _F32, dev),
+          _ptr("topk_idx", topk_idx, T * p.k, _I32, dev), _opt("token_mask", token_mask, T, _BYTE, dev), coef,
+          _ptr("loss", loss, 1, _F32, dev), _ptr("counts", counts, E, _I32, dev),
+          _ptr("mean_prob", mean_prob, E, _F32, dev), _opt("dlogits", dlogits, T * E, _F32, dev), *_ws(ws, dev))
 
 
 def moex_backward_balanced(p: Problem, x, w_router, W1, W2, dy, token_mask, coef, dx, dw_router, dbias, dW1, dW2, loss,
                            counts, mean_prob, ws, stream=None):
-    a, td, w = _Args("moex_backward_balanced"), p.T * p.d_model, p.E * p.d_model * p.d_expert
-    args = (ctypes.byref(p), a("x", x, td, _BF16), a("w_router", w_router, p.d_model * p.E, _BF16),
-            a("W1", W1, w, _BF16), a("W2", W2, w, _BF16), a("dy", dy, td, _BF16),
-            a("token_mask", token_mask, p.T, _BYTE, False), float(coef), a("dx", dx, td, _BF16),
-            a("dw_router", dw_router, p.d_model * p.E, _BF16), a("dbias", dbias, p.E, _F32, False),
-            a("dW1", dW1, w, _BF16), a("dW2", dW2, w, _BF16), a("loss", loss, 1, _F32),
-            a("counts", counts, p.E, _I32, False), a("mean_prob", mean_prob, p.E, _F32, False))
-    a.call(stream, *args, *a.ws(ws))
+    dev, T, d, E = _device("x", x), p.T, p.d_model, p.E
+    td, w = T * d, E * d * p.d_expert
+    _call(_c.moex_backward_balanced, dev, stream, ctypes.byref(p), _ptr("x", x, td, _BF16, dev),
+          _ptr("w_router", w_router, d * E, _BF16, dev), _ptr("W1", W1, w, _BF16, dev), _ptr("W2", W2, w, _BF16, dev),
+          _ptr("dy", dy, td, _BF16, dev), _opt("token_mask", token_mask, T, _BYTE, dev), coef,
+          _ptr("dx", dx, td, _BF16, dev), _ptr("dw_router", dw_router, d * E, _BF16, dev),
+          _opt("dbias", dbias, E, _F32, dev), _ptr("dW1", dW1, w, _BF16, dev), _ptr("dW2", dW2, w, _BF16, dev),
+          _ptr("loss", loss, 1, _F32, dev), _opt("counts", counts, E, _I32, dev),
+          _opt("mean_prob", mean_prob, E, _F32, dev), *_ws(ws, dev))
 
 
 def expert_shapes(p: Problem):
@@ -182,32 +195,30 @@ def expert_shapes(p: Problem):
     return (*shapes(p.d_model, p.d_expert), *shapes(p.d_expert, p.d_model))
 
 
-def _experts(a: _Args, p: Problem, W1q, W1s, W2q, W2s):
+def _experts(p: Problem, W1q, W1s, W2q, W2s, dev):
     n1, n2 = p.E * p.d_expert * code_pitch(p.d_model), p.E * p.d_model * code_pitch(p.d_expert)
-    return (a("W1q", W1q, n1, _CODE), a("W1s", W1s, n1 // 128, _SCALE), a("W2q", W2q, n2, _CODE),
-            a("W2s", W2s, n2 // 128, _SCALE))
+    return (_ptr("W1q", W1q, n1, _CODE, dev), _ptr("W1s", W1s, n1 // 128, _SCALE, dev),
+            _ptr("W2q", W2q, n2, _CODE, dev), _ptr("W2s", W2s, n2 // 128, _SCALE, dev))
 
 
 def moex_quantize_experts(p: Problem, W1, W2, W1q, W1s, W2q, W2s, stream=None):
-    a, w = _Args("moex_quantize_experts"), p.E * p.d_model * p.d_expert
-    args = (ctypes.byref(p), a("W1", W1, w, _rows(p)), a("W2", W2, w, _rows(p)), *_experts(a, p, W1q, W1s, W2q, W2s))
-    a.call(stream, *args)
+    dev, w = _device("W1", W1), p.E * p.d_model * p.d_expert
+    _call(_c.moex_quantize_experts, dev, stream, ctypes.byref(p), _ptr("W1", W1, w, _rows(p), dev),
+          _ptr("W2", W2, w, _rows(p), dev), *_experts(p, W1q, W1s, W2q, W2s, dev))
 
 
 def moex_grouped_ffn_fp8(p: Problem, x8, x_scale, perm, offsets, W1q, W1s, W2q, W2s, y_perm, ws, stream=None):
-    a, R = _Args("moex_grouped_ffn_fp8"), p.T * p.k
-    rows = p.T if perm is not None else R
-    args = (ctypes.byref(p), a("x8", x8, rows * code_pitch(p.d_model), _CODE),
-            a("x_scale", x_scale, rows * scale_pitch(p.d_model), _SCALE), a("perm", perm, R, _I32, False),
-            a("offsets", offsets, p.E + 1, _I32), *_experts(a, p, W1q, W1s, W2q, W2s),
-            a("y_perm", y_perm, R * p.d_model, _BF16))
-    a.call(stream, *args, *a.ws(ws))
+    dev, d, R = _device("x8", x8), p.d_model, p.T * p.k
+    rows = R if perm is None else p.T
+    _call(_c.moex_grouped_ffn_fp8, dev, stream, ctypes.byref(p), _ptr("x8", x8, rows * code_pitch(d), _CODE, dev),
+          _ptr("x_scale", x_scale, rows * scale_pitch(d), _SCALE, dev), _opt("perm", perm, R, _I32, dev),
+          _ptr("offsets", offsets, p.E + 1, _I32, dev), *_experts(p, W1q, W1s, W2q, W2s, dev),
+          _ptr("y_perm", y_perm, R * d, _BF16, dev), *_ws(ws, dev))
 
 
 def moex_forward_fp8(p: Problem, x, x8, x_scale, w_router, router_bias, W1q, W1s, W2q, W2s, y, ws, stream=None):
-    a, td = _Args("moex_forward_fp8"), p.T * p.d_model
-    args = (ctypes.byref(p), a("x", x, td, _BF16), a("x8", x8, p.T * code_pitch(p.d_model), _CODE, False),
-            a("x_scale", x_scale, p.T * scale_pitch(p.d_model), _SCALE, False),
-            a("w_router", w_router, p.d_model * p.E, _BF16), a("router_bias", router_bias, p.E, _F32, False),
-            *_experts(a, p, W1q, W1s, W2q, W2s), a("y", y, td, _BF16))
-    a.call(stream, *args, *a.ws(ws))
+    dev, T, d, E = _device("x", x), p.T, p.d_model, p.E
+    _call(_c.moex_forward_fp8, dev, stream, ctypes.byref(p), _ptr("x", x, T * d, _BF16, dev),
+          _opt("x8", x8, T * code_pitch(d), _CODE, dev), _opt("x_scale", x_scale, T * scale_pitch(d), _SCALE, dev),
+          _ptr("w_router", w_router, d * E, _BF16, dev), _opt("router_bias", router_bias, E, _F32, dev),
+          *_experts(p, W1q, W1s, W2q, W2s, dev), _ptr("y", y, T * d, _BF16, dev), *_ws(ws, dev))

@@ -76,18 +76,18 @@ __device__ __forceinline__ void find_rows(const int32_t* __restrict__ offsets, i
   __syncthreads();
 }
 
-// A workgroup multiplies 32 TM rows by 32 NG columns; wave (g, ks) takes column
+// A workgroup multiplies 32 rows by 32 NG columns; wave (g, ks) takes column
 // group g and every KS-th block of 128 positions, straight from memory into
 // registers, and the KS sums of a group are added in order through LDS.
-template <int TM, int NG, int KS, bool ACT>
+template <int NG, int KS, bool ACT>
 __global__ __launch_bounds__(NG * KS * kWave) void gemm_fp8_small_kernel(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ As, const int32_t* __restrict__ perm, int64_t a_rows,
     const int32_t* __restrict__ offsets, const uint8_t* __restrict__ B, const uint8_t* __restrict__ Bs,
     void* __restrict__ C, uint8_t* __restrict__ Cs, int64_t R, int K, int N, int E, int n_tiles) {
   static_assert(!ACT || NG == 4, "an 8-bit output block spans 128 columns");
-  constexpr int BM = 32 * TM;
+  constexpr int BM = 32;
   __shared__ int s_info[3];
-  __shared__ float s_acc[KS > 1 ? (KS - 1) * NG * TM * 16 * kWave : 1];
+  __shared__ float s_acc[KS > 1 ? (KS - 1) * NG * 16 * kWave : 1];
   __shared__ float s_max[ACT ? NG * BM : 1];
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int g = wave % NG, ks = wave / NG;
@@ -100,113 +100,78 @@ __global__ __launch_bounds__(NG * KS * kWave) void gemm_fp8_small_kernel(
   const int KB = (int)(code_pitch(K) / kQBlock);
   const int64_t cp = code_pitch(K), sp = scale_pitch(K);
   const int half = lane >> 5;
-  const u32x4* pa[TM];
-  const uint8_t* ps[TM];
-#pragma unroll
-  for (int mi = 0; mi < TM; ++mi) {
-    const int64_t r = min(row0 + mi * 32 + (lane & 31), row_end - 1);  // rows past the end repeat the last
-    int64_t src = r;
-    if (perm) {
-      src = perm[r];
-      if (src < 0 || src >= a_rows) src = 0;
-    }
-    pa[mi] = (const u32x4*)(A + src * cp) + half;
-    ps[mi] = As + src * sp;
+  const int64_t row = row0 + (lane & 31);
+  int64_t src = min(row, row_end - 1);  // rows past the end repeat the last
+  if (perm) {
+    src = perm[src];
+    if (src < 0 || src >= a_rows) src = 0;
   }
+  const u32x4* pa = (const u32x4*)(A + src * cp) + half;
+  const uint8_t* ps = As + src * sp;
   const int64_t slab = (int64_t)e * (N / 32) + (cols ? ng : 0);
   const u32x4* pb = (const u32x4*)(B + slab * KB * 4096) + half * 32 + (lane & 31);
   const uint8_t* pbs = Bs + slab * KB * 32 + (lane & 31);
-  f32x16 acc[TM];
+  f32x16 acc;
 #pragma unroll
-  for (int mi = 0; mi < TM; ++mi)
-#pragma unroll
-    for (int v = 0; v < 16; ++v) acc[mi][v] = 0.0f;
+  for (int v = 0; v < 16; ++v) acc[v] = 0.0f;
   if (cols) {
 #pragma unroll 2
     for (int kb = ks; kb < KB; kb += KS) {
-      u32x4 b[4], a[TM][4];
-      int sb = pbs[kb * 32], sa[TM];
+      u32x4 a[4], b[4];
+      const int sa = ps[kb], sb = pbs[kb * 32];
 #pragma unroll
       for (int q = 0; q < 4; ++q) b[q] = pb[(int64_t)kb * 256 + q * 64];
 #pragma unroll
-      for (int mi = 0; mi < TM; ++mi) {
-        sa[mi] = ps[mi][kb];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) a[mi][q] = pa[mi][kb * 8 + q * 2];
-      }
+      for (int q = 0; q < 4; ++q) a[q] = pa[kb * 8 + q * 2];
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int mi = 0; mi < TM; ++mi)
-          acc[mi] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join8(b[2 * j], b[2 * j + 1]),
-                                                                    join8(a[mi][2 * j], a[mi][2 * j + 1]), acc[mi], 0,
-                                                                    0, 0, sb, 0, sa[mi]);
+        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join8(b[2 * j], b[2 * j + 1]),
+                                                              join8(a[2 * j], a[2 * j + 1]), acc, 0, 0, 0, sb, 0, sa);
     }
   }
   if constexpr (KS > 1) {
     if (ks > 0)
 #pragma unroll
-      for (int mi = 0; mi < TM; ++mi)
-#pragma unroll
-        for (int v = 0; v < 16; ++v)
-          s_acc[((((ks - 1) * NG + g) * TM + mi) * 16 + v) * kWave + lane] = acc[mi][v];
+      for (int v = 0; v < 16; ++v) s_acc[(((ks - 1) * NG + g) * 16 + v) * kWave + lane] = acc[v];
     __syncthreads();
     if (ks == 0)
 #pragma unroll
       for (int u = 0; u < KS - 1; ++u)
 #pragma unroll
-        for (int mi = 0; mi < TM; ++mi)
-#pragma unroll
-          for (int v = 0; v < 16; ++v) acc[mi][v] += s_acc[(((u * NG + g) * TM + mi) * 16 + v) * kWave + lane];
+        for (int v = 0; v < 16; ++v) acc[v] += s_acc[((u * NG + g) * 16 + v) * kWave + lane];
   }
   if constexpr (ACT) {
-    if (ks == 0)
-#pragma unroll
-      for (int mi = 0; mi < TM; ++mi) {
-        float m = 0.0f;
-#pragma unroll
-        for (int v = 0; v < 16; ++v) {
-          acc[mi][v] = gelu_tanh(acc[mi][v]);  // 0 stays 0: columns past N
-          m = fmaxf(m, fabsf(acc[mi][v]));
-        }
-        m = fmaxf(m, __shfl_xor(m, 32, kWave));
-        s_max[g * BM + mi * 32 + (lane & 31)] = m;
-      }
-    __syncthreads();
-    if (ks > 0) return;
-    const int64_t hp = code_pitch(N), hs = scale_pitch(N);
-    const int cb = blockIdx.x % n_tiles;  // block of 128 columns
-#pragma unroll
-    for (int mi = 0; mi < TM; ++mi) {
-      const int rl = mi * 32 + (lane & 31);
+    if (ks == 0) {
       float m = 0.0f;
 #pragma unroll
-      for (int u = 0; u < NG; ++u) m = fmaxf(m, s_max[u * BM + rl]);
-      const int byte = scale_byte(m);
-      const float inv = inv_scale(byte);
-      const int64_t r = row0 + rl;
-      if (r >= row_end) continue;
-      uint8_t* out = (uint8_t*)C + r * hp + (int64_t)ng * 32 + 4 * half;
-#pragma unroll
-      for (int v = 0; v < 4; ++v)
-        *(uint32_t*)(out + 8 * v) = encode4(acc[mi][4 * v], acc[mi][4 * v + 1], acc[mi][4 * v + 2],
-                                            acc[mi][4 * v + 3], inv);
-      if (g == 0 && half == 0) Cs[r * hs + cb] = (uint8_t)byte;
-    }
-  } else {
-    if (ks > 0 || !cols) return;
-#pragma unroll
-    for (int mi = 0; mi < TM; ++mi) {
-      const int64_t r = row0 + mi * 32 + (lane & 31);
-      if (r >= row_end) continue;
-      bf16_bits* out = (bf16_bits*)C + r * N + ng * 32 + 4 * half;
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        u32x2 o;
-        o[0] = pack_bf16x2(acc[mi][4 * v], acc[mi][4 * v + 1]);
-        o[1] = pack_bf16x2(acc[mi][4 * v + 2], acc[mi][4 * v + 3]);
-        *(u32x2*)(out + 8 * v) = o;
+      for (int v = 0; v < 16; ++v) {
+        acc[v] = gelu_tanh(acc[v]);  // 0 stays 0: columns past N
+        m = fmaxf(m, fabsf(acc[v]));
       }
+      s_max[g * BM + (lane & 31)] = fmaxf(m, __shfl_xor(m, 32, kWave));
+    }
+    __syncthreads();
+    if (ks > 0) return;
+    float m = 0.0f;
+#pragma unroll
+    for (int u = 0; u < NG; ++u) m = fmaxf(m, s_max[u * BM + (lane & 31)]);
+    if (row >= row_end) return;
+    const int byte = scale_byte(m);
+    const float inv = inv_scale(byte);
+    uint8_t* out = (uint8_t*)C + row * code_pitch(N) + (int64_t)ng * 32 + 4 * half;
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      *(uint32_t*)(out + 8 * v) = encode4(acc[4 * v], acc[4 * v + 1], acc[4 * v + 2], acc[4 * v + 3], inv);
+    if (g == 0 && half == 0) Cs[row * scale_pitch(N) + blockIdx.x % n_tiles] = (uint8_t)byte;
+  } else {
+    if (ks > 0 || !cols || row >= row_end) return;
+    bf16_bits* out = (bf16_bits*)C + row * N + ng * 32 + 4 * half;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      u32x2 o;
+      o[0] = pack_bf16x2(acc[4 * v], acc[4 * v + 1]);
+      o[1] = pack_bf16x2(acc[4 * v + 2], acc[4 * v + 3]);
+      *(u32x2*)(out + 8 * v) = o;
     }
   }
 }
@@ -261,51 +226,70 @@ __device__ __forceinline__ void wait_vmem_all_if0(int all) {
       : "memory", "scc");
 }
 
+// m-tiles of a group of `rows` rows that are not a tail of at most half a tile
+__device__ __forceinline__ int full_m_tiles(int rows) { return rows / L_BM + (rows % L_BM > L_BM / 2 ? 1 : 0); }
+
 template <bool ACT, bool GATHER>
 __global__ __launch_bounds__(L_NW * kWave, 1) void gemm_fp8_kernel(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ As, const int32_t* __restrict__ perm, int64_t a_rows,
     const int32_t* __restrict__ offsets, const uint8_t* __restrict__ B, const uint8_t* __restrict__ Bs,
     void* __restrict__ C, uint8_t* __restrict__ Cs, int64_t R, int K, int N, int E, int n_tiles, int gm) {
   __shared__ __attribute__((aligned(1024))) char smem[2 * L_STAGE + 2 * L_WIN + L_NW * L_EP];
-  __shared__ int s_tstart[257];  // first tile of each expert, and their number
-  __shared__ int s_lo[256], s_hi[256];  // its rows
+  // Tiles of an expert: ceil(rows / 256) m-tiles of n_tiles each. A last m-tile
+  // of at most 128 rows costs less than a whole one; those come after all others,
+  // so that a last, partly filled round of tiles is a cheap one.
+  __shared__ int s_tstart[257], s_tail[257];  // first tile of each expert in either list, and their numbers
+  __shared__ int s_lo[256], s_hi[256];        // its rows
   const int tid = threadIdx.x, lane = tid % kWave, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   if (wave == 0) {
-    int lo4[4], hi4[4], cnt[4], local = 0;
+    int cnt[4], tail[4], local = 0, tlocal = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int e = lane * 4 + i;
-      lo4[i] = hi4[i] = 0;
+      int rows = 0;
       if (e < E) {
-        lo4[i] = max(offsets[e], 0);
-        hi4[i] = (int)min((int64_t)offsets[e + 1], R);
-        s_lo[e] = lo4[i];
-        s_hi[e] = hi4[i];
+        const int lo = max(offsets[e], 0), hi = (int)min((int64_t)offsets[e + 1], R);
+        s_lo[e] = lo;
+        s_hi[e] = hi;
+        rows = max(hi - lo, 0);
       }
-      cnt[i] = hi4[i] > lo4[i] ? (int)ceil_div(hi4[i] - lo4[i], L_BM) * n_tiles : 0;
+      cnt[i] = full_m_tiles(rows) * n_tiles;
+      tail[i] = rows % L_BM > 0 && rows % L_BM <= L_BM / 2 ? n_tiles : 0;
       local += cnt[i];
+      tlocal += tail[i];
     }
-    int incl = local;
+    int incl = local, tincl = tlocal;
 #pragma unroll
     for (int o = 1; o < kWave; o <<= 1) {
-      const int v = __shfl_up(incl, o, kWave);
-      if (lane >= o) incl += v;
+      const int v = __shfl_up(incl, o, kWave), w = __shfl_up(tincl, o, kWave);
+      if (lane >= o) {
+        incl += v;
+        tincl += w;
+      }
     }
-    int run = incl - local;
+    int run = incl - local, trun = tincl - tlocal;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (lane * 4 + i < E) s_tstart[lane * 4 + i] = run;
+      if (lane * 4 + i < E) {
+        s_tstart[lane * 4 + i] = run;
+        s_tail[lane * 4 + i] = trun;
+      }
       run += cnt[i];
+      trun += tail[i];
     }
-    if (lane == kWave - 1) s_tstart[E] = incl;
+    if (lane == kWave - 1) {
+      s_tstart[E] = incl;
+      s_tail[E] = tincl;
+    }
   }
   __syncthreads();
-  const int total = __builtin_amdgcn_readfirstlane(s_tstart[E]);
-  // a contiguous share of the tile list per XCD (workgroups are dealt to the 8 XCDs in turn)
+  // a contiguous share of either tile list per XCD (workgroups are dealt to the 8 XCDs in turn)
   const int xcd = blockIdx.x % 8, nb = gridDim.x / 8, j = blockIdx.x / 8;
-  const int lo = (int)((int64_t)total * xcd / 8), hi = (int)((int64_t)total * (xcd + 1) / 8);
-  const int n_items = hi - lo > j ? (hi - lo - j - 1) / nb + 1 : 0;
+  const int total = __builtin_amdgcn_readfirstlane(s_tstart[E]), tails = __builtin_amdgcn_readfirstlane(s_tail[E]);
+  const int lo = (int)((int64_t)total * xcd / 8), n_full = (int)((int64_t)total * (xcd + 1) / 8) - lo;
+  const int tlo = (int)((int64_t)tails * xcd / 8), n_all = n_full + (int)((int64_t)tails * (xcd + 1) / 8) - tlo;
+  const int n_items = n_all > j ? (n_all - j - 1) / nb + 1 : 0;
   if (n_items == 0) return;
   const int cp = (int)code_pitch(K), sp = (int)scale_pitch(K), KB = cp / kQBlock;  // KB >= 2
   lds_char* const lds = (lds_char*)smem;
@@ -332,18 +316,22 @@ __global__ __launch_bounds__(L_NW * kWave, 1) void gemm_fp8_kernel(
   auto locate = [&](int item) {
     Tile tl = {0, 0, 0, 0};
     if (item >= n_items) return tl;
-    const int t = lo + j + item * nb;
+    const int i0 = j + item * nb;
+    const bool is_tail = i0 >= n_full;
+    const int t = is_tail ? tlo + i0 - n_full : lo + i0;
+    const int* const start = is_tail ? s_tail : s_tstart;
     int e = 0;  // experts after the first that start at or before t
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int q = 1 + i * kWave + lane;
-      e += __popcll(__ballot(q < E && s_tstart[q < E ? q : 0] <= t));
+      e += __popcll(__ballot(q < E && start[q < E ? q : 0] <= t));
     }
     tl.e = __builtin_amdgcn_readfirstlane(e);
     const int first = __builtin_amdgcn_readfirstlane(s_lo[tl.e]), end = __builtin_amdgcn_readfirstlane(s_hi[tl.e]);
-    const int mt = (int)ceil_div(end - first, L_BM);
-    int n_tile, m_idx;
-    tile_coords(t - __builtin_amdgcn_readfirstlane(s_tstart[tl.e]), mt, n_tiles, gm, n_tile, m_idx);
+    const int mt = full_m_tiles(end - first), local = t - __builtin_amdgcn_readfirstlane(start[tl.e]);
+    int n_tile = local;
+    int m_idx = mt;
+    if (!is_tail) tile_coords(local, mt, n_tiles, gm, n_tile, m_idx);
     tl.row0 = first + m_idx * L_BM;
     tl.rows = min(end - tl.row0, L_BM);
     tl.n0 = n_tile * L_BN;
@@ -558,6 +546,10 @@ __global__ __launch_bounds__(L_NW * kWave, 1) void gemm_fp8_kernel(
       if (KB & 1) move_addresses((buf + 1) & 1);
     }
 
+    if (tl.rows <= wm0) {
+      // nothing to store, but the waits below count stores: leave nothing for them to wait for
+      wait_vmem<0>();
+    } else {
     lds_char* const ep = lds + 2 * L_STAGE + 2 * L_WIN + wave * L_EP;
     // 32 rows of 64 bytes at a time: pieces of 16 bytes, XOR-ed by the row
     auto ep_at = [&](int row, int ch) { return ep + row * 64 + ((ch ^ ((row >> 2) & 3)) << 4); };
@@ -629,6 +621,7 @@ __global__ __launch_bounds__(L_NW * kWave, 1) void gemm_fp8_kernel(
           __builtin_amdgcn_sched_barrier(0);
         }
     }
+    }
     tl = nxt;
     buf = (buf + KB) & 1;
     win += nwins;
@@ -672,14 +665,39 @@ __global__ __launch_bounds__(256) void quantize_weights_kernel(const bf16_bits* 
 // m-tiles of BM rows over E groups of R rows in all, at most
 int64_t m_tiles_bound(int64_t R, int E, int bm) { return min(R, (R + (int64_t)E * (bm - 1)) / bm); }
 
-template <int TM, int NG, int KS, bool ACT>
+// Whether a product takes the 256 x 256 tiles rather than workgroups of 32 rows
+// that read the weights straight into registers. The tiles do a matrix
+// instruction's work with an eighth of the weight reads, the small form has no
+// pipeline to fill and eight times the workgroups. Both estimates in us, from
+// times on MI355X over 1 .. 6000 tokens of five layer shapes: a workgroup of the
+// small form costs about 0.7 us per block of 128 positions and 128 columns, four
+// blocks' worth of it before the first; a tile 1.5 us a block and 6 us around
+// them, per round of tiles. Both products of a layer, us, small form / tiles:
+// 8192-wide coarse experts at 8 rows an expert 50 / 102, at 128 220 / 125;
+// 64 fine experts of 2048 x 1024 at 4 rows 50 / 56, at 64 132 / 63; 12 experts of
+// 320 x 448 at 194 rows 17 / 26, at 1500 65 / 31. (Workgroups of 64 and 128 rows
+// were behind one of the two at every size.)
+// MOE_FP8_TILES=0|1 forces the choice where both are possible.
+bool fp8_tiles(int64_t R, int K, int N, int E) {
+  if (K <= kQBlock) return false;  // the tiles' pipeline needs two steps
+  const char* force = getenv("MOE_FP8_TILES");
+  if (force && force[0]) return atoi(force) != 0;
+  const double kb = (double)(code_pitch(K) / kQBlock), cus = device_cus(), busy = (double)min(R, (int64_t)E);
+  const double m_small = max(busy, R / 32.0 + 0.5 * E), m_large = max(busy, (double)R / L_BM + 0.5 * E);
+  const double small = m_small * N / 128.0 * (kb + 4.0) * 0.7 / cus;
+  const double rounds = m_large * ceil_div(N, L_BN) / cus;
+  const double large = (double)(int64_t)(rounds + 0.999) * (1.5 * kb + 6.0);
+  return large < small;
+}
+
+template <int NG, int KS, bool ACT>
 hipError_t launch_small(const void* A, const void* As, const int32_t* perm, int64_t a_rows, const int32_t* offsets,
                         const void* B, const void* Bs, void* C, void* Cs, int64_t R, int K, int N, int E,
                         hipStream_t s) {
   const int n_tiles = (int)ceil_div(N, 32 * NG);
-  const int64_t grid = m_tiles_bound(R, E, 32 * TM) * n_tiles;
+  const int64_t grid = m_tiles_bound(R, E, 32) * n_tiles;
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((gemm_fp8_small_kernel<TM, NG, KS, ACT>), dim3((unsigned)grid), dim3(NG * KS * kWave), 0, s,
+  hipLaunchKernelGGL((gemm_fp8_small_kernel<NG, KS, ACT>), dim3((unsigned)grid), dim3(NG * KS * kWave), 0, s,
                      (const uint8_t*)A, (const uint8_t*)As, perm, a_rows, offsets, (const uint8_t*)B,
                      (const uint8_t*)Bs, C, (uint8_t*)Cs, R, K, N, E, n_tiles);
   return hipGetLastError();
@@ -690,14 +708,14 @@ hipError_t launch_small(const void* A, const void* As, const int32_t* perm, int6
 hipError_t launch_gemm_fp8(const void* A, const void* As, const int32_t* perm, int64_t a_rows, const int32_t* offsets,
                            const void* B, const void* Bs, void* C, void* Cs, int64_t R, int K, int N, int E, bool act,
                            hipStream_t s) {
-  if (R > 40 * (int64_t)E && K > kQBlock) {
+  if (fp8_tiles(R, K, N, E)) {
     const int n_tiles = (int)ceil_div(N, L_BN);
     const int64_t tiles = m_tiles_bound(R, E, L_BM) * n_tiles;
     if (tiles > INT32_MAX) return hipErrorInvalidValue;
     const unsigned grid = (unsigned)max((int64_t)8, min(ceil_div(tiles, 8) * 8, (int64_t)device_cus() / 8 * 8));
-#define MOE_LAUNCH(ACT_, GATHER_)                                                                                 \
-  hipLaunchKernelGGL((gemm_fp8_kernel<ACT_, GATHER_>), dim3(grid), dim3(L_NW * kWave), 0, s, (const uint8_t*)A,     \
-                     (const uint8_t*)As, perm, a_rows, offsets, (const uint8_t*)B, (const uint8_t*)Bs, C,         \
+#define MOE_LAUNCH(ACT_, GATHER_)                                                                                \
+  hipLaunchKernelGGL((gemm_fp8_kernel<ACT_, GATHER_>), dim3(grid), dim3(L_NW * kWave), 0, s, (const uint8_t*)A,  \
+                     (const uint8_t*)As, perm, a_rows, offsets, (const uint8_t*)B, (const uint8_t*)Bs, C,        \
                      (uint8_t*)Cs, R, K, N, E, n_tiles, group_m())
     if (act && perm) MOE_LAUNCH(true, true);
     else if (act) MOE_LAUNCH(true, false);
@@ -705,8 +723,8 @@ hipError_t launch_gemm_fp8(const void* A, const void* As, const int32_t* perm, i
 #undef MOE_LAUNCH
     return hipGetLastError();
   }
-  if (act) return launch_small<1, 4, 4, true>(A, As, perm, a_rows, offsets, B, Bs, C, Cs, R, K, N, E, s);
-  return launch_small<1, 2, 4, false>(A, As, perm, a_rows, offsets, B, Bs, C, Cs, R, K, N, E, s);
+  if (act) return launch_small<4, 4, true>(A, As, perm, a_rows, offsets, B, Bs, C, Cs, R, K, N, E, s);
+  return launch_small<2, 4, false>(A, As, perm, a_rows, offsets, B, Bs, C, Cs, R, K, N, E, s);
 }
 
 hipError_t launch_quantize_weights(const void* w, void* q, void* qs, int E, int K, int N, hipStream_t s) {
