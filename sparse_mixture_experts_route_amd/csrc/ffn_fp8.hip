@@ -226,23 +226,22 @@ __device__ __forceinline__ void wait_vmem_all_if0(int all) {
       : "memory", "scc");
 }
 
+// Tiles of an expert: ceil(rows / 256) m-tiles of n_tiles each. A last m-tile of
+// at most 128 rows costs less than a whole one; those come after all others, so
+// that a last, partly filled round of tiles is a cheap one.
+struct TileList {
+  int start[257], tail[257];  // first tile of each expert among either, and their numbers
+  int lo[256], hi[256];       // its rows
+};
+
 // m-tiles of a group of `rows` rows that are not a tail of at most half a tile
 __device__ __forceinline__ int full_m_tiles(int rows) { return rows / L_BM + (rows % L_BM > L_BM / 2 ? 1 : 0); }
 
-template <bool ACT, bool GATHER>
-__global__ __launch_bounds__(L_NW * kWave, 1) void gemm_fp8_kernel(
-    const uint8_t* __restrict__ A, const uint8_t* __restrict__ As, const int32_t* __restrict__ perm, int64_t a_rows,
-    const int32_t* __restrict__ offsets, const uint8_t* __restrict__ B, const uint8_t* __restrict__ Bs,
-    void* __restrict__ C, uint8_t* __restrict__ Cs, int64_t R, int K, int N, int E, int n_tiles, int gm) {
-  __shared__ __attribute__((aligned(1024))) char smem[2 * L_STAGE + 2 * L_WIN + L_NW * L_EP];
-  // Tiles of an expert: ceil(rows / 256) m-tiles of n_tiles each. A last m-tile
-  // of at most 128 rows costs less than a whole one; those come after all others,
-  // so that a last, partly filled round of tiles is a cheap one.
-  __shared__ int s_tstart[257], s_tail[257];  // first tile of each expert in either list, and their numbers
-  __shared__ int s_lo[256], s_hi[256];        // its rows
-  const int tid = threadIdx.x, lane = tid % kWave, half = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  if (wave == 0) {
+// Wave 0 builds the list; ends with a barrier.
+__device__ __forceinline__ void build_list(const int32_t* __restrict__ offsets, int E, int64_t R, int n_tiles,
+                                           TileList& list) {
+  if (threadIdx.x < kWave) {
+    const int lane = threadIdx.x;
     int cnt[4], tail[4], local = 0, tlocal = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -250,8 +249,8 @@ __global__ __launch_bounds__(L_NW * kWave, 1) void gemm_fp8_kernel(
       int rows = 0;
       if (e < E) {
         const int lo = max(offsets[e], 0), hi = (int)min((int64_t)offsets[e + 1], R);
-        s_lo[e] = lo;
-        s_hi[e] = hi;
+        list.lo[e] = lo;
+        list.hi[e] = hi;
         rows = max(hi - lo, 0);
       }
       cnt[i] = full_m_tiles(rows) * n_tiles;
@@ -272,24 +271,85 @@ __global__ __launch_bounds__(L_NW * kWave, 1) void gemm_fp8_kernel(
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (lane * 4 + i < E) {
-        s_tstart[lane * 4 + i] = run;
-        s_tail[lane * 4 + i] = trun;
+        list.start[lane * 4 + i] = run;
+        list.tail[lane * 4 + i] = trun;
       }
       run += cnt[i];
       trun += tail[i];
     }
     if (lane == kWave - 1) {
-      s_tstart[E] = incl;
-      s_tail[E] = tincl;
+      list.start[E] = incl;
+      list.tail[E] = tincl;
     }
   }
   __syncthreads();
-  // a contiguous share of either tile list per XCD (workgroups are dealt to the 8 XCDs in turn)
+}
+
+// An XCD's contiguous share of either list (workgroups are dealt to the 8 XCDs
+// in turn): n_full tiles from `lo`, then tails from `tlo`, n_all together.
+struct XcdShare {
+  int lo, n_full, tlo, n_all;
+};
+__device__ __forceinline__ XcdShare xcd_share(const TileList& list, int E, int xcd) {
+  const int total = __builtin_amdgcn_readfirstlane(list.start[E]), tails = __builtin_amdgcn_readfirstlane(list.tail[E]);
+  XcdShare s;
+  s.lo = (int)((int64_t)total * xcd / 8);
+  s.n_full = (int)((int64_t)total * (xcd + 1) / 8) - s.lo;
+  s.tlo = (int)((int64_t)tails * xcd / 8);
+  s.n_all = s.n_full + (int)((int64_t)tails * (xcd + 1) / 8) - s.tlo;
+  return s;
+}
+
+// Tile `i` of an XCD's share; every lane of the wave takes part.
+struct TilePlace {
+  int e, n_tile, row0, rows;
+};
+__device__ __forceinline__ TilePlace find_tile(const TileList& list, const XcdShare& share, int E, int i, int n_tiles,
+                                               int gm) {
+  const int lane = threadIdx.x % kWave;
+  const bool is_tail = i >= share.n_full;
+  const int t = is_tail ? share.tlo + i - share.n_full : share.lo + i;
+  const int* const start = is_tail ? list.tail : list.start;
+  int e = 0;  // experts after the first that start at or before t
+#pragma unroll
+  for (int q4 = 0; q4 < 4; ++q4) {
+    const int q = 1 + q4 * kWave + lane;
+    e += __popcll(__ballot(q < E && start[q < E ? q : 0] <= t));
+  }
+  TilePlace p;
+  p.e = __builtin_amdgcn_readfirstlane(e);
+  const int first = __builtin_amdgcn_readfirstlane(list.lo[p.e]), end = __builtin_amdgcn_readfirstlane(list.hi[p.e]);
+  const int mt = full_m_tiles(end - first), local = t - __builtin_amdgcn_readfirstlane(start[p.e]);
+  int m_idx = mt;
+  p.n_tile = local;
+  if (!is_tail) tile_coords(local, mt, n_tiles, gm, p.n_tile, m_idx);
+  p.row0 = first + m_idx * L_BM;
+  p.rows = min(end - p.row0, L_BM);
+  return p;
+}
+
+// Tiles of a last round are cut where that saves at least so many pairs of steps:
+// about 20 us of a product whose partial sums and second launch take 12
+constexpr int kFp8SplitPairs = 6;
+
+template <bool ACT, bool GATHER>
+__global__ __launch_bounds__(L_NW * kWave, 1) void gemm_fp8_kernel(
+    const uint8_t* __restrict__ A, const uint8_t* __restrict__ As, const int32_t* __restrict__ perm, int64_t a_rows,
+    const int32_t* __restrict__ offsets, const uint8_t* __restrict__ B, const uint8_t* __restrict__ Bs,
+    void* __restrict__ C, uint8_t* __restrict__ Cs, int64_t R, int K, int N, int E, int n_tiles, int gm,
+    float* __restrict__ partials, int max_rem) {
+  __shared__ __attribute__((aligned(1024))) char smem[2 * L_STAGE + 2 * L_WIN + L_NW * L_EP];
+  __shared__ TileList list;
+  const int tid = threadIdx.x, lane = tid % kWave, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  build_list(offsets, E, R, n_tiles, list);
   const int xcd = blockIdx.x % 8, nb = gridDim.x / 8, j = blockIdx.x / 8;
-  const int total = __builtin_amdgcn_readfirstlane(s_tstart[E]), tails = __builtin_amdgcn_readfirstlane(s_tail[E]);
-  const int lo = (int)((int64_t)total * xcd / 8), n_full = (int)((int64_t)total * (xcd + 1) / 8) - lo;
-  const int tlo = (int)((int64_t)tails * xcd / 8), n_all = n_full + (int)((int64_t)tails * (xcd + 1) / 8) - tlo;
-  const int n_items = n_all > j ? (n_all - j - 1) / nb + 1 : 0;
+  const XcdShare share = xcd_share(list, E, xcd);
+  // whole tiles, then, of products with a long contraction, at most two parts of
+  // the tiles of a last round, cut between pairs of steps
+  const int pairs = (int)(code_pitch(K) / kQBlock) >> 1;
+  const SplitK sk = split_k(share.n_all, nb, j, pairs, kFp8SplitPairs, max_rem);
+  const int n_items = sk.n_items;
   if (n_items == 0) return;
   const int cp = (int)code_pitch(K), sp = (int)scale_pitch(K), KB = cp / kQBlock;  // KB >= 2
   lds_char* const lds = (lds_char*)smem;
@@ -298,6 +358,7 @@ __global__ __launch_bounds__(L_NW * kWave, 1) void gemm_fp8_kernel(
 
   struct Tile {
     int e, n0, row0, rows;  // rows of the group from row0 on, at most L_BM
+    int kb, kn, slot;       // first step and steps; slot of its partial sums (-1: the tile is whole)
   };
   struct Loads {
     i32x4 rsA, rsB, rsS;
@@ -314,27 +375,22 @@ __global__ __launch_bounds__(L_NW * kWave, 1) void gemm_fp8_kernel(
   const int s_row = (wave & 3) * 64 + lane;
   // tile t; past the workgroup's last item: no rows and no columns
   auto locate = [&](int item) {
-    Tile tl = {0, 0, 0, 0};
+    Tile tl = {0, 0, 0, 0, 0, KB, -1};
     if (item >= n_items) return tl;
-    const int i0 = j + item * nb;
-    const bool is_tail = i0 >= n_full;
-    const int t = is_tail ? tlo + i0 - n_full : lo + i0;
-    const int* const start = is_tail ? s_tail : s_tstart;
-    int e = 0;  // experts after the first that start at or before t
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int q = 1 + i * kWave + lane;
-      e += __popcll(__ballot(q < E && start[q < E ? q : 0] <= t));
+    int i0 = j + item * nb;
+    if (item >= sk.full && sk.rem > 0) {
+      const int r = sk.r_first + item - sk.full;
+      i0 = sk.full * nb + r;
+      const int first = (int)max(sk.s0 - (int64_t)r * pairs, (int64_t)0), last = (int)min(sk.s1 - (int64_t)r * pairs, (int64_t)pairs);
+      tl.kb = 2 * first;
+      tl.kn = (last == pairs ? KB : 2 * last) - tl.kb;
+      if (tl.kn < KB) tl.slot = (int)blockIdx.x * 2 + item - sk.full;
     }
-    tl.e = __builtin_amdgcn_readfirstlane(e);
-    const int first = __builtin_amdgcn_readfirstlane(s_lo[tl.e]), end = __builtin_amdgcn_readfirstlane(s_hi[tl.e]);
-    const int mt = full_m_tiles(end - first), local = t - __builtin_amdgcn_readfirstlane(start[tl.e]);
-    int n_tile = local;
-    int m_idx = mt;
-    if (!is_tail) tile_coords(local, mt, n_tiles, gm, n_tile, m_idx);
-    tl.row0 = first + m_idx * L_BM;
-    tl.rows = min(end - tl.row0, L_BM);
-    tl.n0 = n_tile * L_BN;
+    const TilePlace pl = find_tile(list, share, E, i0, n_tiles, gm);
+    tl.e = pl.e;
+    tl.row0 = pl.row0;
+    tl.rows = pl.rows;
+    tl.n0 = pl.n_tile * L_BN;
     return tl;
   };
   auto load_perm = [&](const Tile& t_, int (&pv)[L_ALD + 1]) {
@@ -383,8 +439,8 @@ __global__ __launch_bounds__(L_NW * kWave, 1) void gemm_fp8_kernel(
       buffer_load_lds16(l.rsB, l.gb, (uint32_t)kt * 4096u + (i - L_ALD) * 1024u,
                         lds_base + 2 * L_A + buf * L_B + wave * 4096 + (i - L_ALD) * 1024);
   };
-  auto issue_window = [&](const Loads& l, int kt, int wbuf) {
-    buffer_load_lds4_if0(kt & 3, l.rsS, l.gs, (uint32_t)(kt >> 2) * (wave < 4 ? 4u : 128u),
+  auto issue_window = [&](const Loads& l, int kt, int wbuf, int now) {
+    buffer_load_lds4_if0(now, l.rsS, l.gs, (uint32_t)(kt >> 2) * (wave < 4 ? 4u : 128u),
                          lds_base + 2 * L_STAGE + wbuf * L_WIN + wave * 256);
   };
 
@@ -455,7 +511,7 @@ __global__ __launch_bounds__(L_NW * kWave, 1) void gemm_fp8_kernel(
   // waited for after the epilogue. Else the next step kt + 1 has to have landed
   // (its scales in window `nwin`) and its first fragments are read here; `stores`
   // is not 0 where an epilogue's stores came after the loads waited for.
-  auto step = [&](const Loads& l, int kt, int buf, int nwin, int fill, int fwin, int stores, auto last_c) {
+  auto step = [&](const Loads& l, int kt, int buf, int nwin, int fill, int fwin, int fnow, int stores, auto last_c) {
     constexpr bool LAST = decltype(last_c)::value;
 #pragma unroll
     for (int ni = 0; ni < L_TN; ++ni)
@@ -475,7 +531,7 @@ __global__ __launch_bounds__(L_NW * kWave, 1) void gemm_fp8_kernel(
 #pragma unroll
       for (int ni = 0; ni < L_TN / 2; ++ni) read_b(0, ni);
     }
-    issue_window(l, fill, fwin);
+    issue_window(l, fill, fwin, fnow);
 #pragma unroll
     for (int ni = L_TN / 2; ni < L_TN; ++ni)
       mfma_pair(1, ni, [&](int mi) {
@@ -486,10 +542,10 @@ __global__ __launch_bounds__(L_NW * kWave, 1) void gemm_fp8_kernel(
       });
     if constexpr (!LAST) take_scales();
   };
-  auto idle_step = [&](const Loads& l, int buf, int fill, int fwin, int stores, bool last) {
+  auto idle_step = [&](const Loads& l, int buf, int fill, int fwin, int fnow, int stores, bool last) {
     if (!last) wait_vmem_all_if0<EP_ST>(stores);
     __syncthreads();
-    issue_window(l, fill, fwin);
+    issue_window(l, fill, fwin, fnow);
 #pragma unroll
     for (int i = 0; i < L_NL; ++i) issue_one(l, fill, buf, i);
   };
@@ -499,13 +555,12 @@ __global__ __launch_bounds__(L_NW * kWave, 1) void gemm_fp8_kernel(
   int npv[L_ALD + 1];
   if constexpr (GATHER) load_perm(tl, npv);
   ld = bind(tl, npv);
-  issue_window(ld, 0, 0);
+  issue_window(ld, tl.kb, 0, 0);
 #pragma unroll
   for (int s2 = 0; s2 < 2; ++s2)
 #pragma unroll
-    for (int i = 0; i < L_NL; ++i) issue_one(ld, s2, s2, i);
-  int buf = 0, win = 0;  // ring buffer and window of the tile's first step
-  const int nwins = (KB + 3) >> 2;
+    for (int i = 0; i < L_NL; ++i) issue_one(ld, tl.kb + s2, s2, i);
+  int buf = 0, win = 0;  // ring buffer and window of the item's first step
 
   for (int item = 0; item < n_items; ++item) {
     // the tile's first stage: its second one, and the last tile's stores, were issued after it
@@ -520,35 +575,49 @@ __global__ __launch_bounds__(L_NW * kWave, 1) void gemm_fp8_kernel(
       for (int ni = 0; ni < L_TN; ++ni)
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[mi][ni][v] = 0.0f;
-    // window of step kt: win + kt / 4; of the next tile's first steps: win + nwins
+    // window of block kb: win + kb / 4 - tl.kb / 4; the next item's first one: win + nwins.
+    // (Items start at even blocks, so a second block never starts a window.)
+    const int end = tl.kb + tl.kn, w0 = win - (tl.kb >> 2), nwins = ((end - 1) >> 2) - (tl.kb >> 2) + 1;
+    const int b0 = buf - tl.kb;  // ring buffer of block kb: (b0 + kb) & 1
     if (tl.rows > wm0) {
-      read_scales(0, win & 1);
+      read_scales(tl.kb, win & 1);
       take_scales();
 #pragma unroll
       for (int mi = 0; mi < L_TM; ++mi) read_a(0, mi);
 #pragma unroll
       for (int ni = 0; ni < L_TN; ++ni) read_b(0, ni);
-      for (int kt = 0; kt < KB - 2; ++kt)
-        step(ld, kt, (buf + kt) & 1, (win + ((kt + 1) >> 2)) & 1, kt + 2, (win + ((kt + 2) >> 2)) & 1,
-             kt == 0 ? item : 0, BoolC<false>{});
+      for (int kb = tl.kb; kb < end - 2; ++kb)
+        step(ld, kb, (b0 + kb) & 1, (w0 + ((kb + 1) >> 2)) & 1, kb + 2, (w0 + ((kb + 2) >> 2)) & 1, (kb + 2) & 3,
+             kb == tl.kb ? item : 0, BoolC<false>{});
       ld = bind(nxt, npv);
-      step(ld, KB - 2, (buf + KB) & 1, (win + ((KB - 1) >> 2)) & 1, 0, (win + nwins) & 1, KB == 2 ? item : 0,
-           BoolC<false>{});
-      step(ld, KB - 1, (buf + KB + 1) & 1, 0, 1, 0, 0, BoolC<true>{});
-      move_addresses((buf + KB) & 1);
+      step(ld, end - 2, (b0 + end) & 1, (w0 + ((end - 1) >> 2)) & 1, nxt.kb, (win + nwins) & 1, 0,
+           tl.kn == 2 ? item : 0, BoolC<false>{});
+      step(ld, end - 1, (b0 + end + 1) & 1, 0, nxt.kb + 1, 0, 1, 0, BoolC<true>{});
+      move_addresses((b0 + end) & 1);
     } else {
       // all of this wave's rows lie past the group's end: its share of the loads alone
-      for (int kt = 0; kt < KB - 2; ++kt)
-        idle_step(ld, (buf + kt) & 1, kt + 2, (win + ((kt + 2) >> 2)) & 1, kt == 0 ? item : 0, false);
+      for (int kb = tl.kb; kb < end - 2; ++kb)
+        idle_step(ld, (b0 + kb) & 1, kb + 2, (w0 + ((kb + 2) >> 2)) & 1, (kb + 2) & 3, kb == tl.kb ? item : 0, false);
       ld = bind(nxt, npv);
-      idle_step(ld, (buf + KB) & 1, 0, (win + nwins) & 1, KB == 2 ? item : 0, false);
-      idle_step(ld, (buf + KB + 1) & 1, 1, 0, 0, true);
-      if (KB & 1) move_addresses((buf + 1) & 1);
+      idle_step(ld, (b0 + end) & 1, nxt.kb, (win + nwins) & 1, 0, tl.kn == 2 ? item : 0, false);
+      idle_step(ld, (b0 + end + 1) & 1, nxt.kb + 1, 0, 1, 0, true);
+      if (tl.kn & 1) move_addresses((buf + 1) & 1);
     }
-
     if (tl.rows <= wm0) {
       // nothing to store, but the waits below count stores: leave nothing for them to wait for
       wait_vmem<0>();
+    } else if (!ACT && tl.slot >= 0) {
+      // part of a tile: its sums in the accumulators' layout, 16 bytes per lane and
+      // register group (more stores than the waits below allow for: only stricter)
+      float* const dst = partials + (int64_t)tl.slot * (L_BM * L_BN) + tid * 4;
+#pragma unroll
+      for (int mi = 0; mi < L_TM; ++mi)
+#pragma unroll
+        for (int ni = 0; ni < L_TN; ++ni)
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            *(f32x4*)(dst + ((mi * L_TN + ni) * 4 + v) * (L_NW * kWave * 4)) =
+                f32x4{acc[mi][ni][4 * v], acc[mi][ni][4 * v + 1], acc[mi][ni][4 * v + 2], acc[mi][ni][4 * v + 3]};
     } else {
     lds_char* const ep = lds + 2 * L_STAGE + 2 * L_WIN + wave * L_EP;
     // 32 rows of 64 bytes at a time: pieces of 16 bytes, XOR-ed by the row
@@ -623,10 +692,72 @@ __global__ __launch_bounds__(L_NW * kWave, 1) void gemm_fp8_kernel(
     }
     }
     tl = nxt;
-    buf = (buf + KB) & 1;
+    buf = (b0 + end) & 1;
     win += nwins;
   }
   wait_vmem<0>();  // the loads past the last tile (of no bytes) have ended before the LDS is given back
+}
+
+// The tiles that were cut: workgroup (x, sub, r0) adds the parts of 32 rows and 128
+// columns of the last round's tiles r0, r0 + gridDim.z, ... of XCD x in the order
+// of their steps, rounds once and stores.
+__global__ __launch_bounds__(4 * kWave) void gemm_fp8_join_kernel(const int32_t* __restrict__ offsets,
+                                                                  const float* __restrict__ partials,
+                                                                  bf16_bits* __restrict__ C, int64_t R, int N, int E,
+                                                                  int n_tiles, int gm, int nb, int pairs,
+                                                                  int max_rem) {
+  __shared__ TileList list;
+  build_list(offsets, E, R, n_tiles, list);
+  const int xcd = blockIdx.x, part = blockIdx.y, lane = threadIdx.x % kWave, ni = threadIdx.x / kWave;
+  const XcdShare share = xcd_share(list, E, xcd);
+  const int full = share.n_all / nb, rem = share.n_all - full * nb;
+  if (!split_leftover(rem, nb, pairs, kFp8SplitPairs, max_rem)) return;
+  const int64_t W = (int64_t)rem * pairs;
+  const int wave = part / L_TM, mi = part % L_TM;  // the GEMM's wave and row group
+  const int wm = wave / L_WN * (L_TM * 32) + mi * 32, wn = wave % L_WN * (L_TN * 32);
+  for (int r = blockIdx.z; r < rem; r += gridDim.z) {
+    const TilePlace pl = find_tile(list, share, E, full * nb + r, n_tiles, gm);
+    const int n = pl.n_tile * L_BN + wn + ni * 32;
+    if (pl.rows <= wm || n >= N) continue;
+    // workgroups j whose pairs [W j / nb, W (j + 1) / nb) meet the tile's [r pairs, (r + 1) pairs)
+    const int64_t u0 = (int64_t)r * pairs, u1 = u0 + pairs;
+    int j0 = (int)(u0 * nb / W), j1 = (int)min((u1 * nb + W - 1) / W, (int64_t)nb);
+    while (W * (j0 + 1) / nb <= u0) ++j0;
+    if (W * j0 / nb <= u0 && W * (j0 + 1) / nb >= u1) continue;  // one workgroup did it all and has stored it
+    const float* const src = partials + (int64_t)(mi * L_TN + ni) * 4 * (L_NW * kWave * 4) + (wave * kWave + lane) * 4;
+    f32x4 acc[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc[v] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = j0; j < j1; j += 4) {  // four parts' loads in flight
+      f32x4 u[4][4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t s0 = W * (j + q) / nb, s1 = W * (j + q + 1) / nb;
+        const bool has = j + q < j1 && s1 > s0 && s0 < u1;
+        const int slot = ((j + q) * 8 + xcd) * 2 + r - (int)(s0 / pairs);
+        const f32x4* const p = (const f32x4*)(src + (has ? (int64_t)slot * (L_BM * L_BN) : 0));
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          u[q][v] = p[v * (L_NW * kWave)];  // of slot 0 when there is no part: dropped
+          if (!has) u[q][v] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[v] += u[q][v];
+    }
+    const int row = wm + (lane & 31);
+    if (row >= pl.rows) continue;
+    bf16_bits* const out = C + (int64_t)(pl.row0 + row) * N + n + 4 * (lane >> 5);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      u32x2 o;
+      o[0] = pack_bf16x2(acc[v][0], acc[v][1]);
+      o[1] = pack_bf16x2(acc[v][2], acc[v][3]);
+      *(u32x2*)(out + 8 * v) = o;
+    }
+  }
 }
 
 // Weights [K, N] of one expert to codes and scales. A workgroup takes 128
@@ -703,24 +834,42 @@ hipError_t launch_small(const void* A, const void* As, const int32_t* perm, int6
   return hipGetLastError();
 }
 
+// persistent workgroups of the tiles: one per CU, as many on every XCD
+unsigned fp8_grid(int64_t R, int N, int E) {
+  const int64_t tiles = m_tiles_bound(R, E, L_BM) * ceil_div(N, L_BN);
+  return (unsigned)max((int64_t)8, min(ceil_div(tiles, 8) * 8, (int64_t)device_cus() / 8 * 8));
+}
+
+// Whether a contraction is long enough for a last round's tiles to be cut.
+bool fp8_splits(int K) { return code_pitch(K) / kQBlock / 2 > kFp8SplitPairs; }
+
 }  // namespace
+
+size_t gemm_fp8_partials_bytes(int64_t R, int K, int N, int E) {
+  if (!fp8_tiles(R, K, N, E) || !fp8_splits(K)) return 0;
+  return (size_t)fp8_grid(R, N, E) * 2 * L_BM * L_BN * sizeof(float);  // two parts per workgroup at most
+}
 
 hipError_t launch_gemm_fp8(const void* A, const void* As, const int32_t* perm, int64_t a_rows, const int32_t* offsets,
                            const void* B, const void* Bs, void* C, void* Cs, int64_t R, int K, int N, int E, bool act,
-                           hipStream_t s) {
+                           float* partials, hipStream_t s) {
   if (fp8_tiles(R, K, N, E)) {
     const int n_tiles = (int)ceil_div(N, L_BN);
-    const int64_t tiles = m_tiles_bound(R, E, L_BM) * n_tiles;
-    if (tiles > INT32_MAX) return hipErrorInvalidValue;
-    const unsigned grid = (unsigned)max((int64_t)8, min(ceil_div(tiles, 8) * 8, (int64_t)device_cus() / 8 * 8));
+    if (m_tiles_bound(R, E, L_BM) * n_tiles > INT32_MAX) return hipErrorInvalidValue;
+    const unsigned grid = fp8_grid(R, N, E);
+    const int nb = (int)grid / 8, pairs = (int)(code_pitch(K) / kQBlock) / 2;
+    const int max_rem = !act && partials && fp8_splits(K) ? nb - 1 : 0;
 #define MOE_LAUNCH(ACT_, GATHER_)                                                                                \
   hipLaunchKernelGGL((gemm_fp8_kernel<ACT_, GATHER_>), dim3(grid), dim3(L_NW * kWave), 0, s, (const uint8_t*)A,  \
                      (const uint8_t*)As, perm, a_rows, offsets, (const uint8_t*)B, (const uint8_t*)Bs, C,        \
-                     (uint8_t*)Cs, R, K, N, E, n_tiles, group_m())
+                     (uint8_t*)Cs, R, K, N, E, n_tiles, group_m(), partials, max_rem)
     if (act && perm) MOE_LAUNCH(true, true);
     else if (act) MOE_LAUNCH(true, false);
     else MOE_LAUNCH(false, false);
 #undef MOE_LAUNCH
+    if (max_rem > 0)
+      hipLaunchKernelGGL(gemm_fp8_join_kernel, dim3(8, L_NW * L_TM, 4), dim3(4 * kWave), 0, s, offsets,
+                         (const float*)partials, (bf16_bits*)C, R, N, E, n_tiles, group_m(), nb, pairs, max_rem);
     return hipGetLastError();
   }
   if (act) return launch_small<4, 4, true>(A, As, perm, a_rows, offsets, B, Bs, C, Cs, R, K, N, E, s);

@@ -180,9 +180,11 @@ hipError_t launch_quantize_weights(const void* w, void* q, void* qs, int E, int 
 // C[r] = A[r] B[e] for rows r of every expert group, 8-bit operands: A codes and
 // scales by rows of K values (row perm[r] of a_rows, or row r), B as
 // launch_quantize_weights writes it. act: C is the 8-bit rows of GELU_tanh
-// (C, Cs), else bf16 [R, N].
+// (C, Cs), else bf16 [R, N], for which `partials` holds gemm_fp8_partials_bytes.
 hipError_t launch_gemm_fp8(const void* A, const void* As, const int32_t* perm, int64_t a_rows, const int32_t* offsets,
                            const void* B, const void* Bs, void* C, void* Cs, int64_t R, int K, int N, int E, bool act,
-                           hipStream_t s);
+                           float* partials, hipStream_t s);
+// Float32 partial-sum bytes of a product without activation (0: none are used)
+size_t gemm_fp8_partials_bytes(int64_t R, int K, int N, int E);
 
 }  // namespace moe

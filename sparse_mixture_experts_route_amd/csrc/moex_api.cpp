@@ -53,6 +53,7 @@ bool fp8_supported(const moe_problem_t& p, bool gathered) {
 
 struct FfnWs {
   uint8_t *h, *hs;  // 8-bit rows of the hidden activations
+  float* partials;  // of the second product's cut tiles
 };
 
 FfnWs carve_ffn(Carver& c, const moe_problem_t& p) {
@@ -60,6 +61,7 @@ FfnWs carve_ffn(Carver& c, const moe_problem_t& p) {
   FfnWs w;
   w.h = c.take<uint8_t>(R * moex_code_pitch(p.d_expert));
   w.hs = c.take<uint8_t>(R * moex_scale_pitch(p.d_expert));
+  w.partials = c.take<float>(gemm_fp8_partials_bytes((int64_t)R, p.d_expert, p.d_model, p.E) / sizeof(float));
   return w;
 }
 
@@ -116,10 +118,10 @@ hipError_t run_ffn(const moe_problem_t& p, const void* x8, const void* xs, const
                    hipStream_t s) {
   const int64_t R = p.T * p.k;
   hipError_t e = launch_gemm_fp8(x8, xs, perm, perm ? p.T : R, offsets, W1q, W1s, w.h, w.hs, R, p.d_model, p.d_expert,
-                                 p.E, true, s);
+                                 p.E, true, nullptr, s);
   if (e == hipSuccess)
     e = launch_gemm_fp8(w.h, w.hs, nullptr, R, offsets, W2q, W2s, y_perm, nullptr, R, p.d_expert, p.d_model, p.E, false,
-                        s);
+                        w.partials, s);
   return e;
 }
 

@@ -56,12 +56,16 @@ CASES = [  # name, d, de, rows per expert, tokens or None (rows already permuted
     ("tall", 128, 64, [700, 300], None),
     ("tiles", 512, 256, [256, 257, 255, 1], 300),
     ("uneven", 256, 640, [600, 3, 0, 90], 200),
+    ("long", 64, 4224, [300, 5, 0, 129], None),
+    ("odd_steps", 192, 1920, [40, 260], 150),
 ]
 
 
+@pytest.mark.parametrize("tiles", ["0", "1"], ids=["small", "tiles"])
 @pytest.mark.parametrize("name,d,de,counts,T", CASES, ids=[c[0] for c in CASES])
-def test_against_float64(moe, name, d, de, counts, T):
-    announce(f"ffn fp8 {name} d={d} de={de} counts={counts}")
+def test_against_float64(moe, monkeypatch, name, d, de, counts, T, tiles):
+    announce(f"ffn fp8 {name} d={d} de={de} counts={counts} tiles={tiles}")
+    monkeypatch.setenv("MOE_FP8_TILES", tiles)
     E, R = len(counts), sum(counts)
     rows = R if T is None else T
     x = randn((rows, d), 1.0, BF, 3)
@@ -90,6 +94,32 @@ def test_against_float64(moe, name, d, de, counts, T):
     assert np.isnan(got[R:]).all()  # rows behind the last group keep what they held
     assert_within(name, got[:R], ref, bound)
     assert torch.equal(y[:R], y2[:R])
+
+
+@pytest.mark.parametrize("counts", [[256] * 33, [2560, 40, 0, 256, 3000], [256 * 31 + 77]],
+                         ids=["one_over", "mixed", "one_expert"])
+def test_cut_tiles_are_joined(moe, monkeypatch, counts):
+    """A contraction long enough that a last round's tiles are cut over the
+    workgroups: the same as the uncut product to float32's rounding of the parts,
+    the same bits twice, and the same in either place of a workspace."""
+    announce(f"ffn fp8 cut tiles {counts}")
+    E, R, d, de = len(counts), sum(counts), 256, 2560
+    p = moe.make_problem(R, d, E, 1, de, BF)
+    x8, xs, _ = quantized(moe, randn((R, d), 1.0, BF, 20))
+    q = experts(moe, p, randn((E, d, de), d ** -0.5, BF, 21), randn((E, de, d), de ** -0.5, BF, 22))
+    off = groups(counts)
+    monkeypatch.setenv("MOE_FP8_TILES", "1")
+    a, b = ffn(moe, p, x8, xs, None, off, q), ffn(moe, p, x8, xs, None, off, q)
+    monkeypatch.setenv("MOE_FP8_TILES", "0")
+    c = ffn(moe, p, x8, xs, None, off, q)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
+    ya, yc = f64(a), f64(c)
+    assert np.isfinite(ya).all()
+    # both round the same hidden rows but for codes at a border (a step of 2^-3 of one of 2560 terms) and
+    # round once to bf16: far apart only where a part was lost or added twice
+    norm = np.linalg.norm(yc, axis=1)
+    assert np.all(np.linalg.norm(ya - yc, axis=1) <= 2.0 ** -6 * norm)
 
 
 def test_row_order_and_batch_do_not_change_a_row(moe):
