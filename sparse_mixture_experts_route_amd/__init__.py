@@ -1,7 +1,7 @@
 """MI355X (gfx950) sparse Mixture-of-Experts layer forward.
 
-Thin Python binding over libmoe.so's C ABI (include/moe.h): the functions
-below carry the C names and only marshal arguments (torch tensors are device
+Thin Python binding over libmoe.so's C ABI (include/moe.h, and include/moe_ext.h
+for the operators around the layer): the functions below carry the C names and only marshal arguments (torch tensors are device
 buffers; their data pointers and torch's current HIP stream go to the
 library). Every step of the layer runs in the library's HIP kernels; there is
 no CPU or PyTorch fallback, and importing fails when the library is missing.
@@ -53,4 +53,4 @@ from ._ext import (  # noqa: F401
     moex_workspace_size,
     scale_pitch,
 )
-from .layer import MoEForward  # noqa: F401
+from .layer import MoEBlockFP8, MoEForward  # noqa: F401

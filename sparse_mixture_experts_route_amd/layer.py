@@ -1,7 +1,8 @@
 """Convenience wrapper: buffers for one layer shape, allocated once with torch.
 
 torch only provides device memory here; the forward itself is the library's
-moe_forward (or the four stage entry points) on the current HIP stream.
+moe_forward (or the four stage entry points) on the current HIP stream, and for
+the block with 8-bit experts moex_add_rmsnorm and moex_forward_fp8.
 """
 
 from __future__ import annotations
@@ -10,7 +11,7 @@ from typing import Optional
 
 import torch
 
-from . import _lib
+from . import _ext, _lib
 
 
 class MoEForward:
@@ -60,3 +61,37 @@ class MoEForward:
         _lib.moe_grouped_ffn(p, out["x_perm"], out["offsets"], W1, W2, out["y_perm"], ws_f, stream)
         _lib.moe_combine(p, out["y_perm"], out["inv"], out["gate"], out["y"], stream)
         return out
+
+
+class MoEBlockFP8:
+    """RMS norm with residual and the layer with 8-bit experts, for a fixed shape.
+
+    The expert weights are quantised once, here. A call adds x to the residual
+    stream, norms it, routes on the 16-bit rows and runs the experts on the 8-bit
+    ones; y and h (the stream after the addition) are this object's buffers.
+    """
+
+    def __init__(self, T: int, d_model: int, E: int, k: int, d_expert: int, gain: torch.Tensor,
+                 w_router: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor,
+                 router_bias: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None):
+        self.problem = p = _lib.make_problem(T, d_model, E, k, d_expert, torch.bfloat16)
+        self.gain, self.w_router, self.router_bias, self.eps = gain, w_router, router_bias, eps
+        dev = W1.device
+
+        def new(shape, dtype):
+            return torch.empty(shape, dtype=dtype, device=dev)
+
+        self.experts = [new(s, torch.uint8) for s in _ext.expert_shapes(p)]
+        _ext.moex_quantize_experts(p, W1, W2, *self.experts, stream)
+        self.ws = new((_ext.moex_workspace_size(p, _ext.MOEX_STAGE_FORWARD_FP8),), torch.uint8)
+        self.h, self.normed, self.y = (new((T, d_model), torch.bfloat16) for _ in range(3))
+        self.x8 = new((T, _ext.code_pitch(d_model)), torch.float8_e4m3fn)
+        self.x_scale = new((T, _ext.scale_pitch(d_model)), torch.uint8)
+
+    def __call__(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None, stream=None):
+        """(y, h): the layer's output, and the stream it is to be added to (x itself without residual)."""
+        p, h = self.problem, self.h if residual is not None else None
+        _ext.moex_add_rmsnorm(p, x, residual, self.gain, self.eps, h, self.normed, self.x8, self.x_scale, None, stream)
+        _ext.moex_forward_fp8(p, self.normed, self.x8, self.x_scale, self.w_router, self.router_bias, *self.experts,
+                              self.y, self.ws, stream)
+        return self.y, h if h is not None else x

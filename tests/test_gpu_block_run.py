@@ -91,6 +91,21 @@ def test_two_blocks_chain(moe):
     assert torch.isfinite(c.y).all()
 
 
+def test_block_class_is_the_two_calls(moe):
+    announce("MoEBlockFP8")
+    T, d, E, k, de = 70, 320, 8, 2, 448
+    b = Block(moe, T, d, E, k, de, 2)
+    m = moe.MoEBlockFP8(T, d, E, k, de, b.gain, b.wr, b.W1, b.W2)
+    x, res = randn((T, d), 1.0, BF, 9), randn((T, d), 1.0, BF, 10)
+    b(x, res)
+    y, h = m(x, res)
+    torch.cuda.synchronize()
+    assert torch.equal(y, b.y) and torch.equal(h, b.h)
+    y2, h2 = m(b.h)  # without a residual the stream is x itself: the same rows, the same result
+    torch.cuda.synchronize()
+    assert h2 is b.h and torch.equal(y2, b.y)
+
+
 @pytest.mark.parametrize("T,d,E,k,de", [(4, 256, 16, 4, 128), (600, 512, 16, 4, 320)])
 def test_graph_replay(moe, T, d, E, k, de):
     announce(f"block graph T={T}")
