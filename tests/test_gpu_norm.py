@@ -172,3 +172,42 @@ def test_quantize_rows(moe, T, d, dt):
     assert np.array_equal(nan, (got & 127) == 127) and nan.sum() >= (2 if T > 1 or d > 1 else 1)
     assert np.array_equal(c[~nan], got[~nan])
     assert np.array_equal(ob.scale_bytes(e, d), xs.cpu().numpy())
+
+
+@pytest.mark.parametrize("T,d,dt", [(17000, 4096, BF), (8200, 4096, F32)], ids=["bf16", "f32"])
+def test_large_arrays_pass_by_the_caches_with_the_same_bits(moe, T, d, dt):
+    """Arrays of 128 MB and more take the streaming form; each half, below that, the plain one."""
+    announce(f"norm large T={T} d={d} {dt}")
+    x, res, gain = randn((T, d), 1.0, dt, 30), randn((T, d), 1.0, dt, 31), randn((d,), 1.0, dt, 32)
+    o = forward(moe, x, res, gain, 1e-5)
+    for half in (slice(0, T // 2), slice(T // 2, T)):
+        part = forward(moe, x[half].contiguous(), res[half].contiguous(), gain, 1e-5)
+        torch.cuda.synchronize()
+        for key in ("h", "y", "scale", "rstd"):
+            assert torch.equal(o[key][half], part[key]), key
+        assert torch.equal(o["y8"][half].view(torch.uint8), part["y8"].view(torch.uint8))
+
+
+def test_other_stream_and_inplace_refusal(moe):
+    """Work goes to the stream given; an output over an input is refused before any of it."""
+    announce("norm stream")
+    T, d = 300, 512
+    x, res, gain = randn((T, d), 1.0, BF, 33), randn((T, d), 1.0, BF, 34), randn((d,), 1.0, BF, 35)
+    want = forward(moe, x, res, gain, 1e-5)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = forward(moe, x, res, gain, 1e-5, stream=s)
+    s.synchronize()
+    assert torch.equal(want["y"], got["y"]) and torch.equal(want["h"], got["h"])
+    p = moe.make_problem(T, d, 1, 1, 64, BF)
+    keep = res.clone()
+    with pytest.raises(moe.MoEError):
+        moe.moex_add_rmsnorm(p, x, res, gain, 1e-5, res, want["y"], None, None, None)
+    with pytest.raises(ValueError):
+        moe.moex_add_rmsnorm(p, x[:, :256], res, gain, 1e-5, want["h"], want["y"], None, None, None)
+    with pytest.raises(ValueError):
+        moe.moex_add_rmsnorm(p, x.t().contiguous().t(), res, gain, 1e-5, want["h"], want["y"], None, None, None)
+    with pytest.raises(TypeError):
+        moe.moex_add_rmsnorm(p, x.float(), res, gain, 1e-5, want["h"], want["y"], None, None, None)
+    torch.cuda.synchronize()
+    assert torch.equal(res, keep)
