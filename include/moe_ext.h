@@ -45,7 +45,8 @@ typedef enum {
   MOEX_STAGE_TRAIN_BALANCED = 4  /* moe_forward_train + moex_backward_balanced */
 } moex_stage_t;
 
-/* Workspace bytes that `stage` needs for problem `p` (host only, no HIP call). */
+/* Workspace bytes that `stage` needs for problem `p` (host only, nothing is enqueued).
+ * A call checks its workspace against the same figure. */
 moe_status_t moex_workspace_size(const moe_problem_t* p, int32_t stage, size_t* bytes);
 
 /* Root-mean-square norm in front of the layer, with the residual's addition
@@ -94,7 +95,7 @@ moe_status_t moex_quantize_rows(const moe_problem_t* p, const void* x, void* x8,
  * its selections, has probability 0 for every expert and gets dlogits 0.
  *   logits [T, E] float32, topk_idx [T, k] int32 (entries outside [0, E) are
  *   ignored), token_mask [T] bytes or NULL, loss [1] float32, counts and
- *   mean_prob as above, dlogits [T, E] float32 or NULL; coef finite
+ *   mean_prob as above, dlogits [T, E] float32 or NULL; coef and coef E finite
  *   ws at least moex_workspace_size(p, MOEX_STAGE_BALANCE) bytes
  * T, E and k of p are used; the other fields must form a valid problem. */
 moe_status_t moex_balance_loss(const moe_problem_t* p, const float* logits, const int32_t* topk_idx,
@@ -104,7 +105,7 @@ moe_status_t moex_balance_loss(const moe_problem_t* p, const float* logits, cons
 /* moe_backward with the balance loss of the same router added to the layer's
  * loss: the gradients of moe_backward for dL/dy = dy plus those of
  * moex_balance_loss through the router, and that loss, its counts and mean_prob.
- * counts, mean_prob and dbias may be NULL, loss may not. Limits of moe_backward.
+ * counts, mean_prob and dbias may be NULL, loss may not; coef as there. Limits of moe_backward.
  *   ws the workspace of the matching moe_forward_train call, of at least
  *      moex_workspace_size(p, MOEX_STAGE_TRAIN_BALANCED) bytes */
 moe_status_t moex_backward_balanced(const moe_problem_t* p, const void* x, const void* w_router, const void* W1,

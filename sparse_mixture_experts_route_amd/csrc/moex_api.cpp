@@ -42,6 +42,9 @@ bool buffers_ok(std::initializer_list<Buf> bufs) {
   return true;
 }
 
+// The gradient's factor coef E has to stay finite: masked rows multiply it by 0.
+bool coef_ok(const moe_problem_t& p, float coef) { return std::isfinite(coef * (float)p.E); }
+
 // Codes of x8, of one expert's weight and of a tile's 256 rows (bf16 rows of
 // the result included) are reached with 32-bit byte offsets.
 bool fp8_supported(const moe_problem_t& p, bool gathered) {
@@ -183,7 +186,7 @@ MOE_API moe_status_t moex_balance_loss(const moe_problem_t* p, const float* logi
                                        float* mean_prob, float* dlogits, void* ws, size_t ws_bytes, void* stream) {
   const moe_status_t st = check_problem(p);
   if (st != MOE_OK) return st;
-  if (!logits || !topk_idx || !loss || !counts || !mean_prob || !ws || !std::isfinite(coef))
+  if (!logits || !topk_idx || !loss || !counts || !mean_prob || !ws || !coef_ok(*p, coef))
     return MOE_ERR_INVALID_ARGUMENT;
   const size_t te = (size_t)p->T * p->E * sizeof(float), need = stage_bytes(*p, MOEX_STAGE_BALANCE);
   if (!buffers_ok({in(logits, te), in(topk_idx, (size_t)p->T * p->k * sizeof(int32_t)), in(token_mask, (size_t)p->T),
@@ -203,7 +206,7 @@ MOE_API moe_status_t moex_backward_balanced(const moe_problem_t* p, const void* 
   const moe_status_t st = check_problem(p);
   if (st != MOE_OK) return st;
   if (!x || !w_router || !W1 || !W2 || !dy || !dx || !dw_router || !dW1 || !dW2 || !loss || !ws ||
-      !std::isfinite(coef))
+      !coef_ok(*p, coef))
     return MOE_ERR_INVALID_ARGUMENT;
   const size_t td = (size_t)p->T * p->d_model * 2, de = (size_t)p->d_model * p->E * 2,
                w = (size_t)p->E * p->d_model * p->d_expert * 2, E = (size_t)p->E * 4;

@@ -198,3 +198,12 @@ def test_binding_checks_tensors(moe):
     with pytest.raises(moe.MoEError):
         moe.moex_workspace_size(p, 17)
     assert moe.code_pitch(320) == 384 and moe.scale_pitch(320) == 16 and moe.scale_pitch(2112) == 32
+
+
+def test_coef_whose_product_with_E_overflows_is_refused(moe, lib):
+    """coef E multiplies the zeros of masked rows: infinity there would be NaN."""
+    n = ctypes.c_size_t(1 << 40)
+    a = [at(i) for i in range(16)]
+    for c in (1e38, -1e38):
+        assert lib.moex_balance_loss(P(moe), a[0], a[1], a[2], f32(c), *a[3:8], n, None) == INVALID
+        assert lib.moex_backward_balanced(P(moe), *a[:6], f32(c), *a[6:15], n, None) == INVALID
