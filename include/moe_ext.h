@@ -134,7 +134,10 @@ moe_status_t moex_quantize_experts(const moe_problem_t* p, const void* W1, const
  *   H[r]      = 8-bit rows of GELU_tanh(X[r] W1[e])
  *   y_perm[r] = H[r] W2[e]                     [T*k, d_model] bf16
  * with X[r] row perm[r] of the T 8-bit rows x8 (perm [T*k] int32 in [0, T)), or
- * row r of T*k of them when perm is NULL. Products accumulate in float32.
+ * row r of T*k of them when perm is NULL. Sums are float32; a matrix instruction
+ * cuts the products it adds at once some 2^-12 below the largest (measured: 1.6e-5
+ * of the result in the root mean square on normal data, where the rounding to
+ * bf16 is off by up to 2^-8).
  *   x8, x_scale  as moex_add_rmsnorm or moex_quantize_rows write them
  *   offsets      [E + 1] int32, non-decreasing, offsets[0] = 0, offsets[E] <= T*k
  *   rows of y_perm outside [0, offsets[E]) are left untouched

@@ -68,12 +68,37 @@ __device__ __forceinline__ void store8(void* base, int64_t piece, const Piece8<B
   }
 }
 
+// dpp of a float or a double
+template <int CTRL, typename S>
+__device__ __forceinline__ S dpp_any(S v) {
+  if constexpr (sizeof(S) == 4) {
+    return dpp<CTRL>(v);
+  } else {
+    u32x2 u = __builtin_bit_cast(u32x2, v);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) u[i] = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u[i], CTRL, 0xF, 0xF, true);
+    return __builtin_bit_cast(S, u);
+  }
+}
+
+// 1 / sqrt(v), v >= 0: the hardware's estimate and one Newton step (which 0 and
+// infinity, whose estimates are exact, skip)
+__device__ __forceinline__ double rsqrt64(double v) {
+  const double r = __builtin_amdgcn_rsq(v);
+  const double n = r * fma(-0.5 * v * r, r, 1.5);
+  return v > 0.0 && v < INFINITY ? n : r;
+}
+
 // Sum over the TPR threads of a row, the same bits in each of them. `slots`
 // holds one value per wave; a barrier separates two uses.
 template <int TPR, typename S>
 __device__ __forceinline__ S row_sum(S v, S* slots) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
+  v += dpp_any<0xB1>(v);   // quad_perm 1, 0, 3, 2
+  v += dpp_any<0x4E>(v);   // quad_perm 2, 3, 0, 1
+  v += dpp_any<0x141>(v);  // row_half_mirror
+  v += dpp_any<0x140>(v);  // row_mirror
+  v += __shfl_xor(v, 16, kWave);
+  v += __shfl_xor(v, 32, kWave);
   if constexpr (TPR > kWave) {
     const int wave = threadIdx.x / kWave, first = threadIdx.x / TPR * (TPR / kWave);
     if (threadIdx.x % kWave == 0) slots[wave] = v;
@@ -98,11 +123,13 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void add_r
   const bool live = t < T;
   if (TPR <= kWave && !live) return;  // a whole wave: no barrier below
   const int64_t row = (live ? t : T - 1) * nvec;
-  Piece8<BF16> in[VPT], res[VPT];
+  constexpr bool EARLY = VPT <= 2;  // gain's load does not wait for the sum; more pieces would cost registers
+  Piece8<BF16> in[VPT], res[VPT], gn[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = i * TPR + j;
     if (c < nvec) {
+      if (EARLY) gn[i] = load8<BF16>(gain, c);
       in[i] = load8<BF16, NT>(x, row + c);
       if (residual) res[i] = load8<BF16, NT>(residual, row + c);
     }
@@ -131,7 +158,7 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void add_r
     }
   }
   ss = row_sum<TPR>(ss, s_sum);
-  const float r = (float)(1.0 / sqrt(ss * inv_d + (double)eps));
+  const float r = (float)rsqrt64(ss * inv_d + (double)eps);
   if (rstd && live && j == 0) rstd[t] = r;
   if (!y && !y8) return;  // the same for every thread
   const int64_t cp = code_pitch((int64_t)nvec * 8), sp = scale_pitch((int64_t)nvec * 8);
@@ -141,7 +168,7 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void add_r
     const int c = i * TPR + j;
     if (c < nvec) {
       float g[8];
-      widen8<BF16>(load8<BF16>(gain, c), g);
+      widen8<BF16>(EARLY ? gn[i] : load8<BF16>(gain, c), g);
 #pragma unroll
       for (int q = 0; q < 8; ++q) v[i][q] = v[i][q] * r * g[q];
       if (y && live) store8<BF16, NT>(y, row + c, narrow8<BF16>(v[i]));
@@ -302,28 +329,32 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void rmsno
   }
 }
 
-// dgain: 64 columns per block, 16 slices of the partial rows added side by
-// side and then in slice order
-constexpr int kDgSlices = 16;
-__global__ __launch_bounds__(64 * kDgSlices) void dgain_kernel(const float* __restrict__ part,
-                                                               float* __restrict__ dgain, int rows, int d) {
-  __shared__ float s_v[kDgSlices][64];
-  const int c = threadIdx.x % 64, sl = threadIdx.x / 64;
-  const int col = blockIdx.x * 64 + c;  // d is a multiple of 64
+// dgain: 16 columns per block, 64 slices of the partial rows added side by side,
+// then 16 by 16 and the four sums, in slice order. (64 columns and 16 slices, a
+// quarter of the workgroups: 4.8 us against 4.6 for 512 partial rows of 2048.)
+constexpr int kDgCols = 16, kDgSlices = 64;
+__global__ __launch_bounds__(kDgCols * kDgSlices) void dgain_kernel(const float* __restrict__ part,
+                                                                    float* __restrict__ dgain, int rows, int d) {
+  __shared__ float s_v[kDgSlices][kDgCols], s_w[4][kDgCols];
+  const int c = threadIdx.x % kDgCols, sl = threadIdx.x / kDgCols;
+  const int col = blockIdx.x * kDgCols + c;  // d is a multiple of 64
   float a = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = sl; i < rows; i += kDgSlices) a += part[(int64_t)i * d + col];
   s_v[sl][c] = a;
   __syncthreads();
-  if (sl == 0) {
+  if (sl < 4) {
     float v = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kDgSlices; ++i) v += s_v[i][c];
-    dgain[col] = v;
+    for (int i = 0; i < kDgSlices / 4; ++i) v += s_v[sl * (kDgSlices / 4) + i][c];
+    s_w[sl][c] = v;
   }
+  __syncthreads();
+  if (sl == 0) dgain[col] = (s_w[0][c] + s_w[1][c]) + (s_w[2][c] + s_w[3][c]);
 }
 
-// Threads per row and pieces per thread by row width (pieces of 8 values).
+// Threads per row and pieces per thread by row width (pieces of 8 values). Four
+// pieces per thread keep the reductions' share small where HBM is the bound.
 #define MOE_NORM_SHAPES(F)                                                                              \
   if (nvec <= 64) { F(64, 1); }                                                                         \
   else if (nvec <= 128) { F(64, 2); }                                                                   \
@@ -333,6 +364,22 @@ __global__ __launch_bounds__(64 * kDgSlices) void dgain_kernel(const float* __re
   else if (nvec <= 2048) { F(512, 4); }                                                                 \
   else { F(1024, 4); }
 
+// The same for few rows, where the bound is the chain of one row: loads, 64-bit
+// sums, the reduction, the stores. One piece per thread shortens it: 8 rows of
+// 7168 bf16 take 3.0 us, four pieces per thread 4.0; 512 rows 6.6 against 7.1;
+// 1024 rows 12.9 against 11.7 (of 2048: 4.6 against 5.4; 4096 rows 13.2 against 12.8).
+#define MOE_NORM_SHAPES_FEW(F)                                                                          \
+  if (nvec <= 64) { F(64, 1); }                                                                         \
+  else if (nvec <= 128) { F(128, 1); }                                                                  \
+  else if (nvec <= 256) { F(256, 1); }                                                                  \
+  else if (nvec <= 512) { F(512, 1); }                                                                  \
+  else if (nvec <= 1024) { F(1024, 1); }                                                                \
+  else if (nvec <= 2048) { F(1024, 2); }                                                                \
+  else { F(1024, 4); }
+
+constexpr int64_t kNormFewRows = 512;
+
+int rows_per_block_few(int nvec) { return nvec <= 64 ? 4 : nvec <= 128 ? 2 : 1; }
 int rows_per_block(int nvec) { return nvec <= 256 ? 4 : nvec <= 512 ? 2 : 1; }
 
 }  // namespace
@@ -345,7 +392,8 @@ int64_t norm_bwd_blocks(int64_t T, int d) {
 hipError_t launch_add_rmsnorm(const moe_problem_t& p, const void* x, const void* residual, const void* gain, float eps,
                               void* h, void* y, void* y8, void* y_scale, float* rstd, hipStream_t s) {
   const int nvec = p.d_model / 8;
-  const int64_t blocks = ceil_div(p.T, rows_per_block(nvec));
+  const bool few = p.T <= kNormFewRows;
+  const int64_t blocks = ceil_div(p.T, few ? rows_per_block_few(nvec) : rows_per_block(nvec));
   const double inv_d = 1.0 / p.d_model;
   if (p.d_model > kNormMaxWidth || blocks > INT32_MAX) return hipErrorInvalidValue;
   // Arrays of 128 MB or more are gone from the last-level cache before the next
@@ -367,7 +415,11 @@ hipError_t launch_add_rmsnorm(const moe_problem_t& p, const void* x, const void*
       else MOE_NORM_LAUNCH(false, TPR, VPT, false);              \
     }                                                            \
   } while (0)
-  MOE_NORM_SHAPES(MOE_NORM)
+  if (few) {
+    MOE_NORM_SHAPES_FEW(MOE_NORM)
+  } else {
+    MOE_NORM_SHAPES(MOE_NORM)
+  }
 #undef MOE_NORM
 #undef MOE_NORM_LAUNCH
   return hipGetLastError();
@@ -394,7 +446,7 @@ hipError_t launch_rmsnorm_backward(const moe_problem_t& p, const void* h, const 
 #undef MOE_NORM
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(dgain_kernel, dim3((unsigned)(p.d_model / 64)), dim3(64 * kDgSlices), 0, s, (const float*)part,
+  hipLaunchKernelGGL(dgain_kernel, dim3((unsigned)(p.d_model / kDgCols)), dim3(kDgCols * kDgSlices), 0, s, (const float*)part,
                      dgain, (int)blocks, p.d_model);
   return hipGetLastError();
 }
