@@ -10,7 +10,14 @@
 // leave from the same registers. 16 neighbouring lanes hold the 128 values of
 // one 8-bit block, so a block's largest magnitude is a reduction within a DPP
 // row. The mean square and r are taken in 64 bits (hidden behind the memory
-// traffic), everything else in float32.
+// traffic), everything else in float32. Codes round the float32 y to e4m3 (half a
+// step, 2^-4), h and y to the rows' type.
+//
+// Measured: 16384 rows of 7168 bf16 with residual, y and 8-bit y 184 us, 5.7 TB/s;
+// forward and backward of 8192 rows of 2048 51 us, 5.3 TB/s of 268 MB, which the
+// last-level cache holds in part; 8 rows of 7168 3.0 us, a chain of latencies.
+// dgain's partial sums, a row per workgroup of the backward launch, are added by
+// a second launch.
 #include "common.h"
 #include "e4m3.h"
 #include "internal.h"
