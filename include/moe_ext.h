@@ -18,7 +18,7 @@
  *          and holds e + 127 for the scale 2^e; bytes past the last block hold 0
  * A value is its code times its block's scale. e is the smallest integer with
  * max|v| <= 448 * 2^e over the block, kept in [-120, 120]; codes are rounded to
- * nearest even from the float32 value. A power of two costs e4m3, a floating
+ * nearest even from the float32 value (moex_add_rmsnorm: from one of more bits). A power of two costs e4m3, a floating
  * format, no relative precision, dividing by it is exact, and the matrix cores
  * apply it while multiplying. A NaN or an infinity becomes a NaN code; an
  * infinity also raises its block's scale to 2^120.

@@ -10,12 +10,12 @@
 // leave from the same registers. 16 neighbouring lanes hold the 128 values of
 // one 8-bit block, so a block's largest magnitude is a reduction within a DPP
 // row. The mean square and r are taken in 64 bits (hidden behind the memory
-// traffic), everything else in float32. Codes round the float32 y to e4m3 (half a
-// step, 2^-4), h and y to the rows' type.
+// traffic), everything else in float32, but where a code depends on more. Codes
+// round y to e4m3 (half a step, 2^-4), h and y are rounded to the rows' type.
 //
-// Measured: 16384 rows of 7168 bf16 with residual, y and 8-bit y 184 us, 5.7 TB/s;
+// Measured: 16384 rows of 7168 bf16 with residual, y and 8-bit y 180 us, 5.9 TB/s;
 // forward and backward of 8192 rows of 2048 51 us, 5.3 TB/s of 268 MB, which the
-// last-level cache holds in part; 8 rows of 7168 3.0 us, a chain of latencies.
+// last-level cache holds in part; 8 rows of 7168 3.1 us, a chain of latencies.
 // dgain's partial sums, a row per workgroup of the backward launch, are added by
 // a second launch.
 #include "common.h"
@@ -86,6 +86,14 @@ __device__ __forceinline__ S dpp_any(S v) {
     for (int i = 0; i < 2; ++i) u[i] = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u[i], CTRL, 0xF, 0xF, true);
     return __builtin_bit_cast(S, u);
   }
+}
+
+// v + lo, |lo| at most half a step of v, to float32 by rounding to odd: a further
+// rounding to fewer bits then gives what v + lo itself would (v alone may sit on a
+// tie that v + lo is beside). 0, infinities and NaN stay.
+__device__ __forceinline__ float to_odd(float v, float lo) {
+  const int b = (int)__float_as_uint(v), differ = (b ^ (int)__float_as_uint(lo)) >> 31;  // -1: lo points to 0
+  return lo != 0.0f && fabsf(lo) < fabsf(v) ? __uint_as_float((uint32_t)((b + differ) | 1)) : v;
 }
 
 // 1 / sqrt(v), v >= 0: the hardware's estimate and one Newton step (which 0 and
@@ -165,7 +173,8 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void add_r
     }
   }
   ss = row_sum<TPR>(ss, s_sum);
-  const float r = (float)rsqrt64(ss * inv_d + (double)eps);
+  const double r64 = rsqrt64(ss * inv_d + (double)eps);
+  const float r = (float)r64, r_lo = (float)(r64 - (double)r);
   if (rstd && live && j == 0) rstd[t] = r;
   if (!y && !y8) return;  // the same for every thread
   const int64_t cp = code_pitch((int64_t)nvec * 8), sp = scale_pitch((int64_t)nvec * 8);
@@ -174,11 +183,31 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void add_r
   for (int i = 0; i < VPT; ++i) {
     const int c = i * TPR + j;
     if (c < nvec) {
-      float g[8];
+      float g[8], h8[8];
       widen8<BF16>(EARLY ? gn[i] : load8<BF16>(gain, c), g);
+      uint32_t near = ~0u;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) v[i][q] = v[i][q] * r * g[q];
+      for (int q = 0; q < 8; ++q) {
+        h8[q] = v[i][q];
+        v[i][q] = v[i][q] * r * g[q];
+        near = min(near, (__float_as_uint(v[i][q]) + 4u) << 13);
+      }
       if (y && live) store8<BF16, NT>(y, row + c, narrow8<BF16>(v[i]));
+      // Codes and scales go by y in more bits than float32 has. That changes them
+      // where y is within 3 of its own steps (three roundings) of a value whose low
+      // 19 bits are 0, as all ties of e4m3 and steps of the scale are: one wave in
+      // 100 does this for random values (8 rows of 7168 3.0 -> 3.1 us, 4096 of 4096 22.6 -> 23.8;
+      // correcting every value 3.6 and 24.9). Without it one code in 10^6 is a step off.
+      if (y8 && __any(near <= 8u << 13)) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          // an infinite gain takes no correction, which would be of either sign
+          const float z = h8[q] * r, z_lo = fmaf(h8[q], r_lo, fmaf(h8[q], r, -z));
+          const float c_lo = fabsf(g[q]) == INFINITY ? 0.0f : z_lo * g[q];
+          const float w = fmaf(z, g[q], c_lo);
+          v[i][q] = to_odd(w, fmaf(z, g[q], -w) + c_lo);
+        }
+      }
     }
     if (y8) {
       float m = 0.0f;
@@ -372,9 +401,10 @@ __global__ __launch_bounds__(kDgCols * kDgSlices) void dgain_kernel(const float*
   else { F(1024, 4); }
 
 // The same for few rows, where the bound is the chain of one row: loads, 64-bit
-// sums, the reduction, the stores. One piece per thread shortens it: 8 rows of
-// 7168 bf16 take 3.0 us, four pieces per thread 4.0; 512 rows 6.6 against 7.1;
-// 1024 rows 12.9 against 11.7 (of 2048: 4.6 against 5.4; 4096 rows 13.2 against 12.8).
+// sums, the reduction, the stores. One piece per thread against four, with the
+// gain loaded behind the sum in both: 8 rows of 7168 bf16 3.5 and 4.2 us. Against
+// four as they are: 512 rows 6.6 and 7.1 us, 1024 rows 12.9 and 11.6 (of 2048
+// 4.6 and 5.4; 4096 rows 13.2 and 12.8).
 #define MOE_NORM_SHAPES_FEW(F)                                                                          \
   if (nvec <= 64) { F(64, 1); }                                                                         \
   else if (nvec <= 128) { F(128, 1); }                                                                  \

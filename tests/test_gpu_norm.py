@@ -211,3 +211,42 @@ def test_other_stream_and_inplace_refusal(moe):
         moe.moex_add_rmsnorm(p, x.float(), res, gain, 1e-5, want["h"], want["y"], None, None, None)
     torch.cuda.synchronize()
     assert torch.equal(res, keep)
+
+
+MANY = [(513, 64), (515, 576), (777, 1088), (514, 2112), (513, 4160), (515, 8256), (513, 16448)]
+
+
+@pytest.mark.parametrize("T,d", MANY)
+def test_forms_of_many_rows(moe, T, d):
+    """More than 512 rows: several pieces per thread, the last of them not in every thread."""
+    announce(f"norm many T={T} d={d}")
+    for dt in (BF, F32) if d < 8000 else (BF,):
+        x, res, gain = randn((T, d), 1.0, dt, 40), randn((T, d), 1.0, dt, 41), randn((d,), 1.0, dt, 42)
+        o = forward(moe, x, res, gain, 1e-5)
+        torch.cuda.synchronize()
+        check_forward(x, res, gain, 1e-5, o)
+
+
+@pytest.mark.parametrize("T,d", [(300, 7168), (1100, 2048)])
+def test_codes_are_those_of_the_unrounded_result(moe, T, d):
+    """bf16 rows and gains put many y next to ties of e4m3: no code may differ from
+    the rounding of the float64 value (y is known to 2^-44, a tie that close does not occur)."""
+    announce(f"norm codes T={T} d={d}")
+    x, res, gain = randn((T, d), 1.0, BF, 50), randn((T, d), 1.0, BF, 51), randn((d,), 1.0, BF, 52)
+    o = forward(moe, x, res, gain, 1e-5)
+    torch.cuda.synchronize()
+    y, _ = ob.rmsnorm(f64(o["h"]), f64(gain), float(np.float32(1e-5)))
+    want, e = ob.encode(ob.pad_to(y, CP(d)))
+    got = codes_of(o["y8"])
+    assert np.array_equal(o["scale"].cpu().numpy()[:, : CP(d) // 128], e + 127)
+    assert np.array_equal(got, want)
+    # infinite and zero gains, rows of zeros: the correction adds nothing of its own
+    gain[:3] = torch.tensor([float("inf"), float("-inf"), 0.0])
+    x[0].zero_()
+    o = forward(moe, x, None, gain, 1e-5)
+    torch.cuda.synchronize()
+    f = o["y"].float()
+    assert torch.isnan(f[0, :2]).all() and not f[0, 2:].any()
+    r = f[1:][x[1:, 0] != 0]
+    assert torch.isinf(r[:, 0]).all() and torch.isfinite(r[:, 2:]).all()
+    assert (o["scale"][1:, 0][x[1:, 0] != 0] == 247).all()
