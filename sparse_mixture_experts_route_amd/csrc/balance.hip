@@ -15,8 +15,13 @@
 // selections of 32 token ranges are counted in LDS (integers: any order gives
 // the same), then every workgroup adds the 32 counts, reads its logits once and
 // writes their gradient. The last workgroup to finish (a ticket) adds the
-// workgroups' probability sums in a fixed order. No float atomics. A batch of one
-// workgroup's size counts for itself: one launch.
+// workgroups' probability sums in a fixed order. No float atomics. A batch of up
+// to four rounds of one workgroup counts for itself: one launch.
+//
+// Statistics are float32 within a row and 64-bit across rows. Measured: 64 tokens
+// of 8 experts 5.2 us of GPU time, 8192 of 64 2.6 + 9, 16384 of 256 with a mask
+// 5.7 + 22 (34 MB, 7 us at the rate of a copy: the rows' arithmetic takes about 9,
+// the counts before it and the ticket after it the rest).
 #include "common.h"
 #include "e4m3.h"
 #include "internal.h"
