@@ -207,3 +207,22 @@ def test_coef_whose_product_with_E_overflows_is_refused(moe, lib):
     for c in (1e38, -1e38):
         assert lib.moex_balance_loss(P(moe), a[0], a[1], a[2], f32(c), *a[3:8], n, None) == INVALID
         assert lib.moex_backward_balanced(P(moe), *a[:6], f32(c), *a[6:15], n, None) == INVALID
+
+
+def test_workspace_of_another_form_is_refused(moe, lib, monkeypatch):
+    """The form of the products is read at every call: a workspace sized for one that needs less is too small."""
+    n = ctypes.c_size_t(0)
+    big = dict(T=4096, d=2048, E=8, k=2, de=8192)
+    monkeypatch.setenv("MOE_FP8_TILES", "0")
+    for stage in (2, 3):
+        assert lib.moex_workspace_size(P(moe, **big), stage, ctypes.byref(n)) == OK
+        size = n.value
+        monkeypatch.setenv("MOE_FP8_TILES", "1")
+        a = [at(i) for i in range(11)]
+        assert lib.moex_workspace_size(P(moe, **big), stage, ctypes.byref(n)) == OK and n.value > size
+        have = ctypes.c_size_t(size)
+        if stage == 2:
+            assert lib.moex_grouped_ffn_fp8(P(moe, **big), *a[:10], have, None) == WS_SMALL
+        else:
+            assert lib.moex_forward_fp8(P(moe, **big), *a, have, None) == WS_SMALL
+        monkeypatch.setenv("MOE_FP8_TILES", "0")
