@@ -34,6 +34,7 @@ namespace {
 constexpr int kCountBlocks = 32;    // token ranges counted side by side
 constexpr int kBalThreads = 1024;
 constexpr int kBalBlocks = 256;     // most workgroups of the second launch
+constexpr int kBalBlocksFew = 128;  // and while that leaves each at most four rounds
 
 // s_c[0 .. E) += selections per expert of tokens [t0, t1), s_c[E] += their valid ones
 __device__ __forceinline__ void count_tokens(const int32_t* __restrict__ idx, const uint8_t* __restrict__ mask,
@@ -44,7 +45,8 @@ __device__ __forceinline__ void count_tokens(const int32_t* __restrict__ idx, co
 #pragma unroll 4
   for (uint32_t i = threadIdx.x; i < n; i += kBalThreads) {
     const int e = p[i];
-    if (e >= 0 && e < E && (!mask || mask[t0 + i / (uint32_t)k])) atomicAdd(&s_c[e], 1);
+    const bool valid = !mask || mask[t0 + i / (uint32_t)k];  // loaded beside e, not behind it
+    if (valid && e >= 0 && e < E) atomicAdd(&s_c[e], 1);
   }
   if (mask) {
     for (int64_t t = t0 + threadIdx.x; t < t1; t += kBalThreads) nv += mask[t] ? 1 : 0;
@@ -103,9 +105,14 @@ __global__ __launch_bounds__(kBalThreads) void balance_main_kernel(
   if constexpr (ALONE) {
     count_tokens(idx, mask, 0, T, k, E, s_c);
   } else {
+    const int step = kBalThreads % (E + 1);
+    int col = tid % (E + 1);
+#pragma unroll 4
     for (int i = tid; i < nparts * (E + 1); i += kBalThreads) {
       const int c = part[i];
-      if (c) atomicAdd(&s_c[i % (E + 1)], c);
+      if (c) atomicAdd(&s_c[col], c);
+      col += step;
+      if (col > E) col -= E + 1;
     }
   }
   __syncthreads();
@@ -233,16 +240,17 @@ __global__ __launch_bounds__(kBalThreads) void balance_main_kernel(
     const int pair = tid % (EW / 2), fs = tid / (EW / 2);
     if (fs < FS) {
       double q0 = 0.0, q1 = 0.0;
+      for (int b0 = fs; b0 < (int)gridDim.x; b0 += kBalBlocksFew)
 #pragma unroll
-      for (int i = 0; i < kBalBlocks / FS; ++i) {
-        const int b = fs + i * FS;
-        uint64_t u = 0;
-        if (b < (int)gridDim.x)
-          u = __hip_atomic_load((const uint64_t*)(psum + (int64_t)b * EW) + pair, __ATOMIC_RELAXED,
-                                __HIP_MEMORY_SCOPE_AGENT);
-        q0 += __uint_as_float((uint32_t)u);
-        q1 += __uint_as_float((uint32_t)(u >> 32));
-      }
+        for (int i = 0; i < kBalBlocksFew / FS; ++i) {
+          const int b = b0 + i * FS;
+          uint64_t u = 0;
+          if (b < (int)gridDim.x)
+            u = __hip_atomic_load((const uint64_t*)(psum + (int64_t)b * EW) + pair, __ATOMIC_RELAXED,
+                                  __HIP_MEMORY_SCOPE_AGENT);
+          q0 += __uint_as_float((uint32_t)u);
+          q1 += __uint_as_float((uint32_t)(u >> 32));
+        }
       s_d[fs * EW + 2 * pair] = q0;
       s_d[fs * EW + 2 * pair + 1] = q1;
     }
@@ -297,6 +305,10 @@ hipError_t launch_balance(const moe_problem_t& p, const float* logits, const int
   // top-8 (64 tokens a round), in one launch against two: 64 tokens 4.7 against
   // 9.0 us, 256 tokens 8.3 against 10.0, 512 tokens 12.9 against 10.2.
   const bool alone = p.T <= (int64_t)4 * (kBalThreads / g);
+  // The last workgroup reads every other one's sums: 128 instead of 256 workgroups
+  // take 16.1 instead of 18.6 us at 4096 tokens of 256 experts, 19.3 instead of 20.5
+  // at 8192, 25.8 instead of 24.6 at 16384 (8 rounds; graph replays of both launches).
+  const int64_t most = p.T <= (int64_t)4 * kBalBlocksFew * (kBalThreads / g) ? kBalBlocksFew : kBalBlocks;
   // at least 64 tokens a range: small batches need few partial counts
   const int64_t per = max(ceil_div(p.T, kCountBlocks), (int64_t)64);
   const int nparts = (int)ceil_div(p.T, per);
@@ -312,7 +324,7 @@ hipError_t launch_balance(const moe_problem_t& p, const float* logits, const int
                      psum, ticket, p.T, p.k, p.E)
 #define MOE_BALANCE(G)                                                                                            \
   case G: {                                                                                                       \
-    const unsigned blocks = (unsigned)min(ceil_div(p.T, kBalThreads / G), (int64_t)kBalBlocks);                   \
+    const unsigned blocks = (unsigned)min(ceil_div(p.T, kBalThreads / G), most);                   \
     if (alone && vec) MOE_BALANCE_LAUNCH(G, true, true);                                                          \
     else if (alone) MOE_BALANCE_LAUNCH(G, false, true);                                                           \
     else if (vec) MOE_BALANCE_LAUNCH(G, true, false);                                                             \
