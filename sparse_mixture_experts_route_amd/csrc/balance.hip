@@ -19,8 +19,8 @@
 // to four rounds of one workgroup counts for itself: one launch.
 //
 // Statistics are float32 within a row and 64-bit across rows. Measured: 64 tokens
-// of 8 experts 5.2 us of GPU time, 8192 of 64 2.6 + 9, 16384 of 256 with a mask
-// 5.7 + 22 (34 MB, 7 us at the rate of a copy: the rows' arithmetic takes about 9,
+// of 8 experts 5.2 us of GPU time, 8192 of 64 3 + 9, 16384 of 256 with a mask
+// 5.5 + 22 (34 MB, 7 us at the rate of a copy: the rows' arithmetic takes about 9,
 // the counts before it and the ticket after it the rest).
 #include "common.h"
 #include "e4m3.h"
@@ -301,9 +301,10 @@ hipError_t launch_balance(const moe_problem_t& p, const float* logits, const int
   float* const psum = (float*)(part + count_ints(p.E));
   const bool vec = p.E % 4 == 0;
   const int g = lanes_per_token(p.E);
-  // Up to four rounds of one workgroup need no second one. Measured at 64 experts,
-  // top-8 (64 tokens a round), in one launch against two: 64 tokens 4.7 against
-  // 9.0 us, 256 tokens 8.3 against 10.0, 512 tokens 12.9 against 10.2.
+  // Up to four rounds of one workgroup need no second one. Measured in graphs at 64
+  // experts, top-8 (64 tokens a round), in one launch against two: 2 rounds 6.0
+  // against 8.2 us, 4 rounds 8.5 and 8.5 (where a launch less is worth its 4 us on
+  // the host), 8 rounds 13.5 against 8.5.
   const bool alone = p.T <= (int64_t)4 * (kBalThreads / g);
   // The last workgroup reads every other one's sums: 128 instead of 256 workgroups
   // take 16.1 instead of 18.6 us at 4096 tokens of 256 experts, 19.3 instead of 20.5
