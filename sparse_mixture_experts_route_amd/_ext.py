@@ -109,6 +109,8 @@ def _ws(ws, dev):
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# without the initialisation check of torch.cuda.current_device: a call holds a GPU tensor by then
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call(f, dev, stream, *args):
@@ -121,7 +123,7 @@ def _call(f, dev, stream, *args):
         stream = stream.cuda_stream
     else:
         stream = int(stream)
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         status = f(*args, stream)
     else:
         with torch.cuda.device(dev):
