@@ -17,7 +17,7 @@
 // forward and backward of 8192 rows of 2048 51 us, 5.3 TB/s of 268 MB, which the
 // last-level cache holds in part; 8 rows of 7168 3.1 us, a chain of latencies.
 // dgain's partial sums, a row per workgroup of the backward launch, are added by
-// a second launch.
+// a second launch; up to 1024 rows its columns have workgroups of their own.
 #include "common.h"
 #include "e4m3.h"
 #include "internal.h"
@@ -257,18 +257,62 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const void* __restri
   }
 }
 
+// Few rows: dgain in the same launch. It needs r, which the call is given, and no
+// sum over a row, so workgroups of their own add 32 columns over all rows: 128 rows
+// side by side, 8 columns a thread. Rows are shared out as without it: dx has the
+// same bits.
+constexpr int kFewThreads = 512, kFewCols = 32;
+template <bool BF16>
+__device__ __forceinline__ void dgain_columns(const void* __restrict__ h, const float* __restrict__ rstd,
+                                              const void* __restrict__ dy, float* __restrict__ dgain, int64_t T,
+                                              int nvec, int col0, float (*s_w)[kFewCols]) {
+  constexpr int CT = kFewCols / 8;  // threads side by side in a row
+  const int c = threadIdx.x % CT, wave = threadIdx.x / kWave;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int64_t t = threadIdx.x / CT; t < T; t += kFewThreads / CT) {
+    float z[8], d[8];
+    widen8<BF16>(load8<BF16>(h, t * nvec + col0 / 8 + c), z);
+    widen8<BF16>(load8<BF16>(dy, t * nvec + col0 / 8 + c), d);
+    const float r = rstd[t];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) acc[q] = fmaf(d[q], z[q] * r, acc[q]);
+  }
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+#pragma unroll
+    for (int o = CT; o < kWave; o <<= 1) acc[q] += __shfl_xor(acc[q], o, kWave);
+    if (threadIdx.x % kWave < CT) s_w[wave][c * 8 + q] = acc[q];
+  }
+  __syncthreads();
+  if (threadIdx.x < kFewCols) {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kFewThreads / kWave; ++w) v += s_w[w][threadIdx.x];
+    dgain[col0 + threadIdx.x] = v;
+  }
+}
+
 // A block takes rows blockIdx, blockIdx + gridDim, ... of its row groups and
 // keeps its share of dgain in registers; the row groups of the block are then
-// added through LDS and leave as one float32 row of `part`.
-template <bool BF16, int TPR, int VPT>
-__global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void rmsnorm_backward_kernel(
+// added through LDS and leave as one float32 row of `part`. FEW: workgroups from
+// `row_blocks` on add dgain by columns, the others leave it out.
+template <bool BF16, int TPR, int VPT, bool FEW>
+__global__ __launch_bounds__(FEW ? kFewThreads : TPR > kNormThreads ? TPR : kNormThreads) void rmsnorm_backward_kernel(
     const void* __restrict__ h, const void* __restrict__ gain, const float* __restrict__ rstd,
     const void* __restrict__ dy, const void* __restrict__ dh, void* __restrict__ dx, float* __restrict__ part,
-    int64_t T, int nvec, float inv_d) {
-  constexpr int THREADS = TPR > kNormThreads ? TPR : kNormThreads;
+    int64_t T, int nvec, float inv_d, int row_blocks) {
+  constexpr int THREADS = FEW ? kFewThreads : TPR > kNormThreads ? TPR : kNormThreads;
   constexpr int RPB = THREADS / TPR;
   __shared__ float s_sum[2][THREADS / kWave];
-  __shared__ float s_acc[RPB > 1 ? TPR * VPT * 8 : 1];
+  __shared__ float s_acc[RPB > 1 && !FEW ? TPR * VPT * 8 : 1];
+  if constexpr (FEW) {  // `part` is dgain
+    __shared__ float s_w[kFewThreads / kWave][kFewCols];
+    if ((int)blockIdx.x >= row_blocks) {
+      dgain_columns<BF16>(h, rstd, dy, part, T, nvec, ((int)blockIdx.x - row_blocks) * kFewCols, s_w);
+      return;
+    }
+  }
   const int j = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   float acc[VPT][8];
 #pragma unroll
@@ -276,7 +320,7 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void rmsno
 #pragma unroll
     for (int q = 0; q < 8; ++q) acc[i][q] = 0.0f;
   int turn = 0;
-  for (int64_t t0 = (int64_t)blockIdx.x * RPB; t0 < T; t0 += (int64_t)gridDim.x * RPB, turn ^= 1) {
+  for (int64_t t0 = (int64_t)blockIdx.x * RPB; t0 < T; t0 += (int64_t)row_blocks * RPB, turn ^= 1) {
     const int64_t t = t0 + grp;
     const bool live = t < T;  // a row group past the end adds zeros and stores nothing
     const int64_t row = t * nvec;
@@ -307,7 +351,7 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void rmsno
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           const float zz = z[q] * r;
-          acc[i][q] = fmaf(d[q], zz, acc[i][q]);
+          if (!FEW) acc[i][q] = fmaf(d[q], zz, acc[i][q]);
           p = fmaf(d[q] * g[q], zz, p);
         }
         s += p;
@@ -335,6 +379,7 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void rmsno
       }
     }
   }
+  if constexpr (FEW) return;
   // the block's row groups in order
   if constexpr (RPB > 1) {
     for (int u = 1; u < RPB; ++u) {
@@ -391,12 +436,14 @@ __global__ __launch_bounds__(kDgCols * kDgSlices) void dgain_kernel(const float*
 
 // Threads per row and pieces per thread by row width (pieces of 8 values). Four
 // pieces per thread keep the reductions' share small where HBM is the bound.
-#define MOE_NORM_SHAPES(F)                                                                              \
+#define MOE_NORM_SHAPES_256(F)                                                                          \
   if (nvec <= 64) { F(64, 1); }                                                                         \
   else if (nvec <= 128) { F(64, 2); }                                                                   \
   else if (nvec <= 256) { F(64, 4); }                                                                   \
   else if (nvec <= 512) { F(128, 4); }                                                                  \
-  else if (nvec <= 1024) { F(256, 4); }                                                                 \
+  else { F(256, 4); }
+#define MOE_NORM_SHAPES(F)                                                                              \
+  if (nvec <= 1024) { MOE_NORM_SHAPES_256(F) }                                                          \
   else if (nvec <= 2048) { F(512, 4); }                                                                 \
   else { F(1024, 4); }
 
@@ -415,6 +462,12 @@ __global__ __launch_bounds__(kDgCols * kDgSlices) void dgain_kernel(const float*
   else { F(1024, 4); }
 
 constexpr int64_t kNormFewRows = 512;
+
+// dgain in the launch of dx (h and dy are read twice, from the caches) or by partial
+// sums and a second launch, us in a graph: 1 row of 7168 bf16 3.5 / 6.3, 512 of 2048
+// 4.2 / 7.9, 1024 of 7168 22.0 / 22.0, 777 of 320 float32 5.6 / 5.5 (and a launch less
+// on the host); 2048 of 2048 bf16 15.0 / 12.4, 4096 of 320 17.0 / 6.3.
+bool norm_bwd_few(const moe_problem_t& p) { return p.T <= 1024 && p.d_model <= 8192; }
 
 int rows_per_block_few(int nvec) { return nvec <= 64 ? 4 : nvec <= 128 ? 2 : 1; }
 int rows_per_block(int nvec) { return nvec <= 256 ? 4 : nvec <= 512 ? 2 : 1; }
@@ -467,20 +520,33 @@ hipError_t launch_rmsnorm_backward(const moe_problem_t& p, const void* h, const 
                                    hipStream_t s) {
   const int nvec = p.d_model / 8;
   if (p.d_model > kNormMaxWidth) return hipErrorInvalidValue;
-  const int64_t blocks = norm_bwd_blocks(p.T, p.d_model);
   const float inv_d = 1.0f / (float)p.d_model;
+#define MOE_NORM_LAUNCH(BF16, TPR, VPT, FEW, GRID, THREADS, OUT)                                                  \
+  hipLaunchKernelGGL((rmsnorm_backward_kernel<BF16, TPR, VPT, FEW>), dim3((unsigned)(GRID)), dim3(THREADS), 0, s, h, \
+                     gain, rstd, dy, dh, dx, OUT, p.T, nvec, inv_d, (int)blocks)
+  if (norm_bwd_few(p)) {
+    const int64_t blocks = ceil_div(p.T, kFewThreads / kNormThreads * rows_per_block(nvec));
+#define MOE_NORM(TPR, VPT)                                                                                    \
+  do {                                                                                                        \
+    if (p.dtype == MOE_DTYPE_BF16)                                                                            \
+      MOE_NORM_LAUNCH(true, TPR, VPT, true, blocks + p.d_model / kFewCols, kFewThreads, dgain);                     \
+    else                                                                                                      \
+      MOE_NORM_LAUNCH(false, TPR, VPT, true, blocks + p.d_model / kFewCols, kFewThreads, dgain);                    \
+  } while (0)
+    MOE_NORM_SHAPES_256(MOE_NORM)
+#undef MOE_NORM
+    return hipGetLastError();
+  }
+  const int64_t blocks = norm_bwd_blocks(p.T, p.d_model);
 #define MOE_NORM(TPR, VPT)                                                                                       \
   do {                                                                                                           \
-    const dim3 b(TPR > kNormThreads ? TPR : kNormThreads);                                                       \
-    if (p.dtype == MOE_DTYPE_BF16)                                                                               \
-      hipLaunchKernelGGL((rmsnorm_backward_kernel<true, TPR, VPT>), dim3((unsigned)blocks), b, 0, s, h, gain,    \
-                         rstd, dy, dh, dx, part, p.T, nvec, inv_d);                                              \
-    else                                                                                                         \
-      hipLaunchKernelGGL((rmsnorm_backward_kernel<false, TPR, VPT>), dim3((unsigned)blocks), b, 0, s, h, gain,   \
-                         rstd, dy, dh, dx, part, p.T, nvec, inv_d);                                              \
+    constexpr int threads = TPR > kNormThreads ? TPR : kNormThreads;                                             \
+    if (p.dtype == MOE_DTYPE_BF16) MOE_NORM_LAUNCH(true, TPR, VPT, false, blocks, threads, part);                \
+    else MOE_NORM_LAUNCH(false, TPR, VPT, false, blocks, threads, part);                                         \
   } while (0)
   MOE_NORM_SHAPES(MOE_NORM)
 #undef MOE_NORM
+#undef MOE_NORM_LAUNCH
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(dgain_kernel, dim3((unsigned)(p.d_model / kDgCols)), dim3(kDgCols * kDgSlices), 0, s, (const float*)part,

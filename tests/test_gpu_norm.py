@@ -250,3 +250,10 @@ def test_codes_are_those_of_the_unrounded_result(moe, T, d):
     r = f[1:][x[1:, 0] != 0]
     assert torch.isinf(r[:, 0]).all() and torch.isfinite(r[:, 2:]).all()
     assert (o["scale"][1:, 0][x[1:, 0] != 0] == 247).all()
+
+
+@pytest.mark.parametrize("T,d", [(1100, 320), (1090, 1088), (1030, 2112), (1026, 4160), (1025, 8192)])
+def test_backward_of_many_rows(moe, T, d):
+    """More than 1024 rows: dgain by partial sums and a second launch."""
+    for dt in (BF, F32) if d < 4000 else (BF,):
+        test_backward(moe, T, d, dt, True)
