@@ -201,11 +201,9 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void add_r
       if (y8 && __any(near <= 8u << 13)) {
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          // an infinite gain takes no correction, which would be of either sign
           const float z = h8[q] * r, z_lo = fmaf(h8[q], r_lo, fmaf(h8[q], r, -z));
-          const float c_lo = fabsf(g[q]) == INFINITY ? 0.0f : z_lo * g[q];
-          const float w = fmaf(z, g[q], c_lo);
-          v[i][q] = to_odd(w, fmaf(z, g[q], -w) + c_lo);
+          const float c_lo = z_lo * g[q], w = fmaf(z, g[q], c_lo);
+          if (fabsf(v[i][q]) < INFINITY) v[i][q] = to_odd(w, fmaf(z, g[q], -w) + c_lo);
         }
       }
     }

@@ -257,3 +257,16 @@ def test_backward_of_many_rows(moe, T, d):
     """More than 1024 rows: dgain by partial sums and a second launch."""
     for dt in (BF, F32) if d < 4000 else (BF,):
         test_backward(moe, T, d, dt, True)
+
+
+def test_rows_whose_root_overflows_keep_their_infinities(moe):
+    """eps 0 and rows of 1e-42: r is past float32, y infinite, its block at the largest scale."""
+    announce("norm infinite r")
+    x = torch.full((3, 256), 1e-42, dtype=F32, device="cuda")
+    x[1] = 1.0
+    o = forward(moe, x, None, torch.ones(256, dtype=F32, device="cuda"), 0.0)
+    torch.cuda.synchronize()
+    for t in (0, 2):
+        assert torch.isinf(o["rstd"][t]) and torch.isinf(o["y"][t]).all() and (o["scale"][t, :2] == 247).all()
+        assert torch.isnan(o["y8"][t].float()).all()
+    assert (o["y"][1] == 1).all() and (o["scale"][1, :2] == 119).all()
