@@ -68,7 +68,9 @@ class MoEBlockFP8:
 
     The expert weights are quantised once, here. A call adds x to the residual
     stream, norms it, routes on the 16-bit rows and runs the experts on the 8-bit
-    ones; y and h (the stream after the addition) are this object's buffers.
+    ones; y and h (the stream after the addition) are this object's buffers, so a
+    residual or x may be another block's h but not, with a residual, this one's
+    (refused: outputs overlap no input).
     """
 
     def __init__(self, T: int, d_model: int, E: int, k: int, d_expert: int, gain: torch.Tensor,
