@@ -257,7 +257,10 @@ moe_status_t moe_forward_train(const moe_problem_t* p, const void* x, const void
  *   mean_prob [E] float32 or NULL  mean router probability per expert
  * The last two are the ingredients of a load-balancing loss, whose formula
  * the pages do not give. Products accumulate in float32; the intermediates
- * (dYp, dU, dX, router logit gradients) are rounded to bf16 between GEMMs. */
+ * (dYp, dU, dX, router logit gradients) are rounded to bf16 between GEMMs.
+ * Limits of moe_forward_train and, each as bf16 under 2 GiB: the T*k rows of
+ * d_model and of d_expert values, one expert's weight, w_router, and T rows of E
+ * values, E rounded up to a multiple of 64; otherwise MOE_ERR_UNSUPPORTED. */
 moe_status_t moe_backward(const moe_problem_t* p, const void* x, const void* w_router,
                           const void* W1, const void* W2, const void* dy, void* dx,
                           void* dw_router, float* dbias, void* dW1, void* dW2,

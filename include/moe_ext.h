@@ -105,7 +105,8 @@ moe_status_t moex_balance_loss(const moe_problem_t* p, const float* logits, cons
 /* moe_backward with the balance loss of the same router added to the layer's
  * loss: the gradients of moe_backward for dL/dy = dy plus those of
  * moex_balance_loss through the router, and that loss, its counts and mean_prob.
- * counts, mean_prob and dbias may be NULL, loss may not; coef as there. Limits of moe_backward.
+ * counts, mean_prob and dbias may be NULL, loss may not; coef as there. The limits
+ * are those of moe_backward.
  *   ws the workspace of the matching moe_forward_train call, of at least
  *      moex_workspace_size(p, MOEX_STAGE_TRAIN_BALANCED) bytes */
 moe_status_t moex_backward_balanced(const moe_problem_t* p, const void* x, const void* w_router, const void* W1,

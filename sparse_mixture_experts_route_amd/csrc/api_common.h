@@ -67,8 +67,9 @@ inline moe_status_t hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK :
 
 // moe_forward_train's and moe_backward's workspace, in bytes
 size_t train_ws_bytes(const moe_problem_t& p);
-// Whether the training path takes problem p
+// Whether the training forward takes problem p, and whether the backward does
 bool train_supported(const moe_problem_t& p);
+bool backward_supported(const moe_problem_t& p);
 
 // The balance loss that a backward pass adds to the layer's loss (moe_ext.h);
 // ws: balance_ws_ints(p) int32

@@ -330,6 +330,14 @@ MOE_API moe_status_t moe_forward(const moe_problem_t* p, const void* x, const vo
 // Training path: bf16, x addressable by the gathering GEMMs, k <= 8, E a multiple of 8.
 bool moe::train_supported(const moe_problem_t& p) { return gather_supported(p) && p.k <= 8 && p.E % 8 == 0; }
 
+// The backward's products reach both operands with 31-bit byte offsets: rows of
+// dYp and H, of dU, of the logits' gradient, one expert's weight and the router's.
+bool moe::backward_supported(const moe_problem_t& p) {
+  const int64_t lim = (int64_t)1 << 30, R = p.T * p.k, d = p.d_model, de = p.d_expert;  // 2 GiB of bf16
+  return train_supported(p) && R * d < lim && R * de < lim && d * de < lim && p.T * padded_experts(p) < lim &&
+         d * p.E < lim;
+}
+
 size_t moe::train_ws_bytes(const moe_problem_t& p) { return stage_bytes(p, MOE_STAGE_TRAIN); }
 
 MOE_API moe_status_t moe_forward_train(const moe_problem_t* p, const void* x, const void* w_router,
@@ -423,7 +431,7 @@ MOE_API moe_status_t moe_backward(const moe_problem_t* p, const void* x, const v
       !aligned16(dx) || !aligned16(dw_router) || !aligned16(dW1) || !aligned16(dW2) || !aligned16(ws) ||
       (dbias && !aligned16(dbias)) || (load_frac && !aligned16(load_frac)) || (mean_prob && !aligned16(mean_prob)))
     return MOE_ERR_INVALID_ARGUMENT;
-  if (!train_supported(*p)) return MOE_ERR_UNSUPPORTED;
+  if (!backward_supported(*p)) return MOE_ERR_UNSUPPORTED;
   if (ws_bytes < stage_bytes(*p, MOE_STAGE_TRAIN)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   return hip_status(run_backward(*p, x, w_router, W1, W2, dy, dx, dw_router, dbias, dW1, dW2, load_frac, mean_prob, ws,
                                  nullptr, (hipStream_t)stream));

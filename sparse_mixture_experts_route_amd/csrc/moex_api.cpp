@@ -210,7 +210,7 @@ MOE_API moe_status_t moex_backward_balanced(const moe_problem_t* p, const void* 
     return MOE_ERR_INVALID_ARGUMENT;
   const size_t td = (size_t)p->T * p->d_model * 2, de = (size_t)p->d_model * p->E * 2,
                w = (size_t)p->E * p->d_model * p->d_expert * 2, E = (size_t)p->E * 4;
-  if (!train_supported(*p)) return MOE_ERR_UNSUPPORTED;
+  if (!backward_supported(*p)) return MOE_ERR_UNSUPPORTED;
   const size_t need = stage_bytes(*p, MOEX_STAGE_TRAIN_BALANCED);
   if (!buffers_ok({in(x, td), in(w_router, de), in(W1, w), in(W2, w), in(dy, td), in(token_mask, (size_t)p->T),
                    out(dx, td), out(dw_router, de), out(dbias, E), out(dW1, w), out(dW2, w), out(loss, sizeof(float)),
