@@ -18,10 +18,13 @@
 // workgroups' probability sums in a fixed order. No float atomics. A batch of up
 // to four rounds of one workgroup counts for itself: one launch.
 //
-// Statistics are float32 within a row and 64-bit across rows. Measured: 64 tokens
-// of 8 experts 5.2 us of GPU time, 8192 of 64 3 + 9, 16384 of 256 with a mask
-// 5.5 + 22 (34 MB, 7 us at the rate of a copy: the rows' arithmetic takes about 9,
-// the counts before it and the ticket after it the rest).
+// Statistics are float32 within a row and 64-bit across rows, so that the means'
+// error does not grow with the batch; what a workgroup sends to the last one is
+// rounded to float32 once, half a unit of its sum, as the mean itself is.
+//
+// Measured: 64 tokens of 8 experts 5.2 us of GPU time, 8192 of 64 3 + 9, 16384 of
+// 256 with a mask 5.5 + 22 (34 MB, 7 us at the rate of a copy: the rows' arithmetic
+// takes about 9, the counts before it and the ticket after it the rest).
 #include "common.h"
 #include "e4m3.h"
 #include "internal.h"
@@ -96,7 +99,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_main_kernel(
     int64_t T, int k, int E) {
   constexpr int TPB = kBalThreads / G;  // tokens side by side
   __shared__ int s_c[257];
-  __shared__ float s_p[TPB * 4 * G];
+  __shared__ __attribute__((aligned(16))) double s_p[TPB * 4 * G];
   __shared__ double s_d[16 * 4 * G > kBalThreads ? 16 * 4 * G : kBalThreads];
   __shared__ int s_last;
   const int tid = threadIdx.x;
@@ -131,7 +134,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_main_kernel(
   }
   const auto vmax = [](float a, float b) { return fmaxf(a, b); };
   const auto vadd = [](float a, float b) { return a + b; };
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  double acc[4] = {0.0, 0.0, 0.0, 0.0};
   // a token's logits and mask, loaded a round ahead (those of masked tokens are dropped)
   struct Row {
     float v[4];
