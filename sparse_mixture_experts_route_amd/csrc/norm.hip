@@ -134,7 +134,7 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void add_r
   constexpr int THREADS = TPR > kNormThreads ? TPR : kNormThreads;
   __shared__ double s_sum[THREADS / kWave];
   const int j = threadIdx.x % TPR;  // place in the row
-  int64_t t = (int64_t)blockIdx.x * (THREADS / TPR) + threadIdx.x / TPR;
+  const int64_t t = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (THREADS / TPR) + threadIdx.x / TPR;
   const bool live = t < T;
   if (TPR <= kWave && !live) return;  // a whole wave: no barrier below
   const int64_t row = (live ? t : T - 1) * nvec;
@@ -483,14 +483,17 @@ hipError_t launch_add_rmsnorm(const moe_problem_t& p, const void* x, const void*
   const bool few = p.T <= kNormFewRows;
   const int64_t blocks = ceil_div(p.T, few ? rows_per_block_few(nvec) : rows_per_block(nvec));
   const double inv_d = 1.0 / p.d_model;
-  if (p.d_model > kNormMaxWidth || blocks > INT32_MAX) return hipErrorInvalidValue;
+  if (p.d_model > kNormMaxWidth) return hipErrorInvalidValue;
+  // A launch takes less than 2^32 threads along x (2^26 rows of up to 2048 values):
+  // at most 2^21 workgroups there, the others along y.
+  const int64_t gy = ceil_div(blocks, (int64_t)1 << 21), gx = ceil_div(blocks, gy);
   // Arrays of 128 MB or more are gone from the last-level cache before the next
   // operator reads them: past the caches, 16384 rows of 7168 bf16 with residual
   // and both outputs take 185 instead of 192 us (5.7 TB/s), while at 8192 rows of
   // 2048 (32 MB arrays) a forward and backward pass take 57 instead of 52 us.
   const bool nt = (double)p.T * p.d_model * (p.dtype == MOE_DTYPE_BF16 ? 2 : 4) >= (double)(128 << 20);
 #define MOE_NORM_LAUNCH(BF16, TPR, VPT, NT)                                                                      \
-  hipLaunchKernelGGL((add_rmsnorm_kernel<BF16, TPR, VPT, NT>), dim3((unsigned)blocks),                           \
+  hipLaunchKernelGGL((add_rmsnorm_kernel<BF16, TPR, VPT, NT>), dim3((unsigned)gx, (unsigned)gy),                 \
                      dim3(TPR > kNormThreads ? TPR : kNormThreads), 0, s, x, residual, gain, eps, h, y,          \
                      (uint8_t*)y8, (uint8_t*)y_scale, rstd, p.T, nvec, inv_d)
 #define MOE_NORM(TPR, VPT)                                       \
