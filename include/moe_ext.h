@@ -122,7 +122,8 @@ moe_status_t moex_backward_balanced(const moe_problem_t* p, const void* x, const
  *   scales [E][N / 32][KB][32]: one byte per column and block of 128 positions
  * (blocks of the 8-bit row format along the contraction; positions past K hold
  * zero codes). W1q, W1s, W2q, W2s hold moex_weight_bytes / moex_weight_scale_bytes
- * of (E, d_model, d_expert) and (E, d_expert, d_model). bf16 problems only. */
+ * of (E, d_model, d_expert) and (E, d_expert, d_model). bf16 problems only;
+ * MOE_ERR_UNSUPPORTED also when an expert's weight reaches 2^37 values. */
 static inline size_t moex_weight_bytes(int64_t E, int64_t K, int64_t N) { return (size_t)(E * N) * moex_code_pitch(K); }
 static inline size_t moex_weight_scale_bytes(int64_t E, int64_t K, int64_t N) {
   return (size_t)(E * N) * (moex_code_pitch(K) / 128);
@@ -144,7 +145,8 @@ moe_status_t moex_quantize_experts(const moe_problem_t* p, const void* W1, const
  *   rows of y_perm outside [0, offsets[E]) are left untouched
  *   ws at least moex_workspace_size(p, MOEX_STAGE_FFN_FP8) bytes
  * bf16 problems only; MOE_ERR_UNSUPPORTED also when the codes of x8, or those of
- * one expert's weight, reach 2 GiB, or a width 2^22. */
+ * one expert's weight, reach 2 GiB, a width 2^22, or T*k rows of a width 2^42
+ * values (in pieces of 32 rows of an expert and 64 columns, 2^31 of them). */
 moe_status_t moex_grouped_ffn_fp8(const moe_problem_t* p, const void* x8, const void* x_scale, const int32_t* perm,
                                   const int32_t* offsets, const void* W1q, const void* W1s, const void* W2q,
                                   const void* W2s, void* y_perm, void* ws, size_t ws_bytes, void* stream);

@@ -108,11 +108,13 @@ __global__ __launch_bounds__(NG * KS * kWave) void gemm_fp8_small_kernel(
   __shared__ float s_max[ACT ? NG * BM : 1];
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int g = wave % NG, ks = wave / NG;
-  find_rows<BM>(offsets, E, R, blockIdx.x / n_tiles, s_info);
+  const uint32_t tile = blockIdx.y * gridDim.x + blockIdx.x, m_tile = tile / (uint32_t)n_tiles;
+  const int n_tile = (int)(tile - m_tile * (uint32_t)n_tiles);
+  find_rows<BM>(offsets, E, R, (int)m_tile, s_info);
   const int e = s_info[0];
   if (e < 0) return;  // the whole workgroup
   const int64_t row0 = s_info[1], row_end = s_info[2];
-  const int ng = (blockIdx.x % n_tiles) * NG + g;  // column group
+  const int ng = n_tile * NG + g;  // column group
   const bool cols = ng * 32 < N;
   const int KB = (int)(code_pitch(K) / kQBlock);
   const int64_t cp = code_pitch(K), sp = scale_pitch(K);
@@ -179,7 +181,7 @@ __global__ __launch_bounds__(NG * KS * kWave) void gemm_fp8_small_kernel(
 #pragma unroll
     for (int v = 0; v < 4; ++v)
       *(uint32_t*)(out + 8 * v) = encode4(acc[4 * v], acc[4 * v + 1], acc[4 * v + 2], acc[4 * v + 3], inv);
-    if (g == 0 && half == 0) Cs[row * scale_pitch(N) + blockIdx.x % n_tiles] = (uint8_t)byte;
+    if (g == 0 && half == 0) Cs[row * scale_pitch(N) + n_tile] = (uint8_t)byte;
   } else {
     if (ks > 0 || !cols || row >= row_end) return;
     bf16_bits* out = (bf16_bits*)C + row * N + ng * 32 + 4 * half;
@@ -853,9 +855,10 @@ hipError_t launch_small(const void* A, const void* As, const int32_t* perm, int6
                         hipStream_t s) {
   const int n_tiles = (int)ceil_div(N, 32 * NG);
   const int64_t grid = m_tiles_bound(R, E, 32) * n_tiles;
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((gemm_fp8_small_kernel<NG, KS, ACT>), dim3((unsigned)grid), dim3(NG * KS * kWave), 0, s,
-                     (const uint8_t*)A, (const uint8_t*)As, perm, a_rows, offsets, (const uint8_t*)B,
+  // a launch takes less than 2^32 threads along x: the other workgroups go along y
+  const int64_t gy = ceil_div(grid, (int64_t)1 << 21), gx = ceil_div(grid, gy);
+  hipLaunchKernelGGL((gemm_fp8_small_kernel<NG, KS, ACT>), dim3((unsigned)gx, (unsigned)gy), dim3(NG * KS * kWave), 0,
+                     s, (const uint8_t*)A, (const uint8_t*)As, perm, a_rows, offsets, (const uint8_t*)B,
                      (const uint8_t*)Bs, C, (uint8_t*)Cs, R, K, N, E, n_tiles);
   return hipGetLastError();
 }
@@ -871,6 +874,8 @@ bool fp8_splits(int K) { return code_pitch(K) / kQBlock / 2 > kFp8SplitPairs; }
 
 }  // namespace
 
+bool gemm_fp8_fits(int64_t R, int N, int E) { return m_tiles_bound(R, E, 32) * ceil_div(N, 64) <= INT32_MAX; }
+
 size_t gemm_fp8_partials_bytes(int64_t R, int K, int N, int E) {
   if (!fp8_tiles(R, K, N, E) || !fp8_splits(K)) return 0;
   return (size_t)fp8_grid(R, N, E) * 2 * L_BM * L_BN * sizeof(float);  // two parts per workgroup at most
@@ -879,9 +884,9 @@ size_t gemm_fp8_partials_bytes(int64_t R, int K, int N, int E) {
 hipError_t launch_gemm_fp8(const void* A, const void* As, const int32_t* perm, int64_t a_rows, const int32_t* offsets,
                            const void* B, const void* Bs, void* C, void* Cs, int64_t R, int K, int N, int E, bool act,
                            float* partials, hipStream_t s) {
+  if (!gemm_fp8_fits(R, N, E)) return hipErrorInvalidValue;
   if (fp8_tiles(R, K, N, E)) {
     const int n_tiles = (int)ceil_div(N, L_BN);
-    if (m_tiles_bound(R, E, L_BM) * n_tiles > INT32_MAX) return hipErrorInvalidValue;
     const unsigned grid = fp8_grid(R, N, E);
     const int nb = (int)grid / 8, pairs = (int)(code_pitch(K) / kQBlock) / 2;
     const int max_rem = !act && partials && fp8_splits(K) ? nb - 1 : 0;
@@ -902,10 +907,13 @@ hipError_t launch_gemm_fp8(const void* A, const void* As, const int32_t* perm, i
   return launch_small<2, 4, false>(A, As, perm, a_rows, offsets, B, Bs, C, Cs, R, K, N, E, s);
 }
 
+// less than 2^32 threads along x
+bool quantize_weights_fits(int K, int N) { return code_pitch(K) / kQBlock * (N / 64) < (int64_t)1 << 24; }
+
 hipError_t launch_quantize_weights(const void* w, void* q, void* qs, int E, int K, int N, hipStream_t s) {
+  if (!quantize_weights_fits(K, N)) return hipErrorInvalidValue;
   const int KB = (int)(code_pitch(K) / kQBlock);
   const int64_t grid = (int64_t)KB * (N / 64);
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
   hipLaunchKernelGGL(quantize_weights_kernel, dim3((unsigned)grid, (unsigned)E), dim3(256), 0, s, (const bf16_bits*)w,
                      (uint8_t*)q, (uint8_t*)qs, K, N, KB);
   return hipGetLastError();

@@ -176,11 +176,15 @@ hipError_t launch_balance(const moe_problem_t& p, const float* logits, const int
                           float coef, float* loss, int32_t* counts, float* mean_prob, float* dlogits, int32_t* ws,
                           hipStream_t s);
 // codes and scales of w [E, K, N] bf16 in the matrix-core layout of moe_ext.h
+// Whether its launch holds K x N values of an expert
+bool quantize_weights_fits(int K, int N);
 hipError_t launch_quantize_weights(const void* w, void* q, void* qs, int E, int K, int N, hipStream_t s);
 // C[r] = A[r] B[e] for rows r of every expert group, 8-bit operands: A codes and
 // scales by rows of K values (row perm[r] of a_rows, or row r), B as
 // launch_quantize_weights writes it. act: C is the 8-bit rows of GELU_tanh
 // (C, Cs), else bf16 [R, N], for which `partials` holds gemm_fp8_partials_bytes.
+// Refuses what gemm_fp8_fits refuses: pieces of 32 rows and 64 columns that pass 31 bits.
+bool gemm_fp8_fits(int64_t R, int N, int E);
 hipError_t launch_gemm_fp8(const void* A, const void* As, const int32_t* perm, int64_t a_rows, const int32_t* offsets,
                            const void* B, const void* Bs, void* C, void* Cs, int64_t R, int K, int N, int E, bool act,
                            float* partials, hipStream_t s);

@@ -46,12 +46,14 @@ bool buffers_ok(std::initializer_list<Buf> bufs) {
 bool coef_ok(const moe_problem_t& p, float coef) { return std::isfinite(coef * (float)p.E); }
 
 // Codes of x8, of one expert's weight and of a tile's 256 rows (bf16 rows of
-// the result included) are reached with 32-bit byte offsets.
+// the result included) are reached with 32-bit byte offsets. (Those of x8 only
+// through a permutation: without one the limit is the interface's, the same for both.)
+// The second product's pieces fit where the first's rows do: T k d_model < 2^31 * 256.
 bool fp8_supported(const moe_problem_t& p, bool gathered) {
   const int64_t rows = gathered ? p.T : p.T * p.k;
   const int64_t lim = INT32_MAX, cd = (int64_t)moex_code_pitch(p.d_model), ce = (int64_t)moex_code_pitch(p.d_expert);
   return p.dtype == MOE_DTYPE_BF16 && rows * cd < lim && p.d_expert * cd < lim && p.d_model * ce < lim &&
-         512 * cd < lim && 512 * ce < lim;
+         512 * cd < lim && 512 * ce < lim && gemm_fp8_fits(p.T * p.k, p.d_expert, p.E);
 }
 
 struct FfnWs {
@@ -234,7 +236,8 @@ MOE_API moe_status_t moex_quantize_experts(const moe_problem_t* p, const void* W
                    out(W1s, moex_weight_scale_bytes(E, d, de)), out(W2q, moex_weight_bytes(E, de, d)),
                    out(W2s, moex_weight_scale_bytes(E, de, d))}))
     return MOE_ERR_INVALID_ARGUMENT;
-  if (p->dtype != MOE_DTYPE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (p->dtype != MOE_DTYPE_BF16 || !quantize_weights_fits(d, de) || !quantize_weights_fits(de, d))
+    return MOE_ERR_UNSUPPORTED;
   hipError_t e = launch_quantize_weights(W1, W1q, W1s, E, d, de, (hipStream_t)stream);
   if (e == hipSuccess) e = launch_quantize_weights(W2, W2q, W2s, E, de, d, (hipStream_t)stream);
   return hip_status(e);

@@ -38,3 +38,15 @@ PAST = [  # the first size that a product of the backward cannot address, and on
 def test_backward_refuses_what_its_products_cannot_address(moe, lib, past, below, balanced):
     assert backward_status(lib, moe, balanced, **below) == WS_SMALL
     assert backward_status(lib, moe, balanced, **past) == UNSUPPORTED
+
+
+def test_experts_refuse_what_their_launches_cannot_hold(moe, lib):
+    """Before the first product, or the first weight, is enqueued."""
+    a = [at(i << 16) for i in range(11)]  # 1 PiB apart
+    one = ctypes.c_size_t(1)
+    wide = dict(T=(1 << 24) - 1, k=128, E=128, d=128, de=1 << 21)  # 2^52 hidden values
+    for size, want in ((wide, UNSUPPORTED), (dict(wide, T=1 << 13), WS_SMALL)):
+        assert lib.moex_grouped_ffn_fp8(P(moe, **size), *a[:10], one, None) == want
+        assert lib.moex_forward_fp8(P(moe, **size), *a, one, None) == want
+    n = 1 << 19  # 2^38 values of an expert
+    assert lib.moex_quantize_experts(P(moe, E=1, k=1, d=n, de=n), *a[:6], None) == UNSUPPORTED
