@@ -506,11 +506,18 @@ hipError_t launch_add_rmsnorm(const moe_problem_t& p, const void* x, const void*
       else MOE_NORM_LAUNCH(false, TPR, VPT, false);              \
     }                                                            \
   } while (0)
-  if (few) {
-    MOE_NORM_SHAPES_FEW(MOE_NORM)
+#define MOE_NORM_FEW(TPR, VPT)                                            \
+  do {                                                                    \
+    if (p.dtype == MOE_DTYPE_BF16) MOE_NORM_LAUNCH(true, TPR, VPT, false); \
+    else MOE_NORM_LAUNCH(false, TPR, VPT, false);                         \
+  } while (0)
+  if (few) {  // 64 MB at most: never past the caches
+    static_assert(kNormFewRows * kNormMaxWidth * 4 < (128 << 20), "few rows take the plain form alone");
+    MOE_NORM_SHAPES_FEW(MOE_NORM_FEW)
   } else {
     MOE_NORM_SHAPES(MOE_NORM)
   }
+#undef MOE_NORM_FEW
 #undef MOE_NORM
 #undef MOE_NORM_LAUNCH
   return hipGetLastError();
