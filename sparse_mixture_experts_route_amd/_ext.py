@@ -113,16 +113,20 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _call(f, dev, stream, *args):
-    """Calls f on GPU dev and on `stream` (None: that GPU's current stream)."""
+def _handle(dev, stream):
+    """HIP handle of `stream` (None: GPU dev's current stream)."""
     if stream is None:
-        stream = _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
-    elif isinstance(stream, torch.cuda.Stream):
+        return _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
+    if isinstance(stream, torch.cuda.Stream):
         if stream.device.index != dev:
             raise ValueError(f"the stream is on {stream.device}, the tensors on GPU {dev}")
-        stream = stream.cuda_stream
-    else:
-        stream = int(stream)
+        return stream.cuda_stream
+    return int(stream)
+
+
+def _call(f, dev, stream, *args):
+    """Calls f on GPU dev and on `stream` (None: that GPU's current stream)."""
+    stream = _handle(dev, stream)
     if dev == _current_device():
         status = f(*args, stream)
     else:
