@@ -235,7 +235,7 @@ constexpr int L_ALD = L_NL / 2;
 // instructions before it would sink behind it.
 __device__ __forceinline__ void buffer_load_lds4_if0(int now, i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
   asm volatile(
-      "s_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 .Lmoe_win%=\n\ts_mov_b32 m0, %1\n\t"
+      "s_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 .Lmoe_win%=\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
       "buffer_load_dword %2, %3, %4 offen lds\n.Lmoe_win%=:"
       :
       : "s"(now), "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)

@@ -36,11 +36,12 @@ __device__ __forceinline__ i32x4 buffer_rsrc(const void* base, uint32_t bytes) {
 // writes bytes [16 i, 16 i + 16) after the wave-uniform LDS address lds.
 // Issued as inline assembly so that the compiler does not wait on it before
 // unrelated LDS reads; the caller waits (vmcnt) before the barrier that
-// publishes the data.
+// publishes the data. A load into LDS reads M0 one wait state after its write at
+// the earliest, which the compiler sees to for its own loads only.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void buffer_load_lds16(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
                : "memory", "m0");
