@@ -107,3 +107,26 @@ def test_refusals_come_first(moe, inputs):
     w[2] = w[2].cpu()
     with pytest.raises(ValueError, match="GPU"):
         moe.MoEBlockFP8(T, D, E, K, DE, *w)
+
+
+def test_made_inside_a_capture(moe, inputs, want):
+    """Then the graph lays the weights out again at every replay."""
+    announce("block made in a capture")
+    gain, wr, W1, W2 = inputs["w"]
+    w1, w2 = W1.clone(), W2.clone()
+    made(moe, inputs)(inputs["x"], inputs["res"])  # kernels loaded before the capture
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, h = moe.MoEBlockFP8(T, D, E, K, DE, gain, wr, w1, w2)(inputs["x"], inputs["res"])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want[0]) and torch.equal(h, want[1])
+    w2.mul_(2)  # exact in 8 bits too: the scales double, and so does every product
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y.float(), 2 * want[0].float())
+    w2.copy_(W2)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want[0])
