@@ -21,13 +21,16 @@
 // Roundings: rows, weights and hidden activations to e4m3 (half a step, 2^-4), the
 // result to bf16. Sums are float32; the instruction cuts the products it adds at
 // once some 2^-12 below the largest (1.6e-5 of a dot product of normal data in the
-// root mean square), less than the 2^-8 of the result's bf16.
+// root mean square), less than the 2^-8 of the result's bf16. Hidden values that this
+// carries over the border of two codes take the result from 0.0017 of it, the rounding
+// to bf16 alone, to 0.0018 .. 0.0020.
 //
 // Measured on MI355X, where a large 8-bit library product reaches 2.9 PFLOP/s and
-// a large copy 5.0 TB/s, both products together: 1 token, 64 experts of 2048 x
-// 1024, top-8 13.8 us; 32 tokens, 8 experts of 2048 x 8192 51 us (5.3 TB/s of
-// weights); 8192 tokens of the fine experts 344 us (1.6 PFLOP/s), 4096 tokens of
-// the coarse ones 295 us (1.9 PFLOP/s).
+// a large copy 5.0 TB/s, both products together, on weights that change from call
+// to call: 1 token, 64 experts of 2048 x 1024, top-8 14.7 us; 32 tokens, 8 experts of
+// 2048 x 8192 58 us (4.7 TB/s of weights; 51 us on the same weights again, which the
+// last-level cache holds in part); 8192 tokens of the fine experts 344 to 351 us (1.6
+// PFLOP/s), 4096 tokens of the coarse ones 294 to 308 us (1.8 to 1.9).
 #include <stdlib.h>
 
 #include "common.h"
@@ -92,7 +95,8 @@ __device__ __forceinline__ void find_rows(const int32_t* __restrict__ offsets, i
 // registers, and the KS sums of a group are added in order through LDS.
 // Bound by the weights' bytes (8 tokens of 64 experts of 7168 x 2048, top-8: 210 us,
 // 5.5 TB/s), for few of them by the chain offsets, row numbers, rows, sums (one
-// token of 2048 x 1024 10 + 5 us). 1, 2 or 4 waves along the contraction are within
+// token of 2048 x 1024 10 + 5 us: the first product's 128 columns, those of a scale
+// block, leave it 64 workgroups for 256 CUs, the second one has 256). 1, 2 or 4 waves along the contraction are within
 // 4% of each other at 1 to 777 tokens but for wide experts' second product (8192:
 // 1 wave 64 us, 4 waves 50); loading the next weights ahead in registers costs the
 // second workgroup of a CU (one token 13.5 -> 18.1 us).
@@ -218,7 +222,10 @@ __global__ __launch_bounds__(NG * KS * kWave) void gemm_fp8_small_kernel(
 // rate; 1.33 without the stage loads: matrix instructions and fragment reads, 256 KB
 // of LDS traffic a step; 1.25 to 1.66 the loads alone, by how many of them miss the
 // L2). The GELU epilogue is 6 to 8 us of a tile, its exponential and reciprocal at a
-// quarter of the vector rate. Four waves of 128 x 128, half stages in a ring of
+// quarter of the vector rate. Without GELU the stores cost nearly as much: the second
+// product of 8192 tokens of the fine experts, 9 rounds of tiles of 8 steps and 268 MB
+// of result, takes 187 us, with its stores dropped 151 (126 of steps, 3 a round
+// around them). Four waves of 128 x 128, half stages in a ring of
 // four, wave groups a phase apart and prefetching the weights into the L2 all ended
 // at the same step or above it.
 constexpr int L_BM = 256, L_BN = 256, L_NW = 8, L_WN = 2, L_TM = 2, L_TN = 4;
@@ -790,7 +797,9 @@ __global__ __launch_bounds__(4 * kWave) void gemm_fp8_join_kernel(const int32_t*
 
 // Weights [K, N] of one expert to codes and scales. A workgroup takes 128
 // positions of 64 columns: rows of 64 bf16 are read whole, transposed through
-// LDS, and 16 codes of a column leave as one 16-byte piece.
+// LDS, and 16 codes of a column leave as one 16-byte piece. Called once per set of
+// weights: 1.3 TB/s (64 experts of 2048 x 1024 0.62 ms, 256 of 7168 x 2048 16.7 ms), 2
+// bytes a lane and load.
 __global__ __launch_bounds__(256) void quantize_weights_kernel(const bf16_bits* __restrict__ w, uint8_t* __restrict__ q,
                                                                uint8_t* __restrict__ qs, int K, int N, int KB) {
   __shared__ float s_w[kQBlock][65];
@@ -828,7 +837,7 @@ int64_t m_tiles_bound(int64_t R, int E, int bm) { return min(R, (R + (int64_t)E 
 // that read the weights straight into registers. The tiles do a matrix
 // instruction's work with an eighth of the weight reads, the small form has no
 // pipeline to fill and eight times the workgroups. Both estimates in us, from
-// times on MI355X over 1 .. 6000 tokens of five layer shapes: a workgroup of the
+// times on MI355X over 1 .. 6000 tokens of five layer shapes (three below): a workgroup of the
 // small form costs about 0.7 us per block of 128 positions and 128 columns, four
 // blocks' worth of it before the first; a tile 1.5 us a block and 6 us around
 // them, per round of tiles. Both products of a layer, us, small form / tiles:

@@ -13,9 +13,11 @@
 // traffic), everything else in float32, but where a code depends on more. Codes
 // round y to e4m3 (half a step, 2^-4), h and y are rounded to the rows' type.
 //
-// Measured: 16384 rows of 7168 bf16 with residual, y and 8-bit y 180 us, 5.9 TB/s;
+// Measured: 16384 rows of 7168 bf16 with residual, y and 8-bit y 181 us, 5.8 TB/s;
 // forward and backward of 8192 rows of 2048 51 us, 5.3 TB/s of 268 MB, which the
-// last-level cache holds in part; 8 rows of 7168 3.1 us, a chain of latencies.
+// last-level cache holds in part (61 us on inputs that change from call to call);
+// 8 rows of 7168 3.1 us, a chain of latencies; 8-bit rows alone of 16384 rows of 7168
+// 66 us, 5.4 TB/s.
 // dgain's partial sums, a row per workgroup of the backward launch, are added by
 // a second launch; up to 1024 rows its columns have workgroups of their own.
 #include "common.h"
@@ -293,7 +295,10 @@ __device__ __forceinline__ void dgain_columns(const void* __restrict__ h, const 
 
 // A block takes rows blockIdx, blockIdx + gridDim, ... of its row groups and
 // keeps its share of dgain in registers; the row groups of the block are then
-// added through LDS and leave as one float32 row of `part`. FEW: workgroups from
+// added through LDS and leave as one float32 row of `part`. 1024 threads of a row
+// wider than 16384 have 128 registers each, too few for h, dy, dh and the sums: 25
+// spill in bf16 and 68 in float32, and 4096 rows of 32768 take 325 and 603 us (3.3 and
+// 3.6 TB/s) where 16384 take 128 and 234 (4.2 and 4.6). FEW: workgroups from
 // `row_blocks` on add dgain by columns, the others leave it out.
 template <bool BF16, int TPR, int VPT, bool FEW>
 __global__ __launch_bounds__(FEW ? kFewThreads : TPR > kNormThreads ? TPR : kNormThreads) void rmsnorm_backward_kernel(
@@ -489,8 +494,8 @@ hipError_t launch_add_rmsnorm(const moe_problem_t& p, const void* x, const void*
   const int64_t gy = ceil_div(blocks, (int64_t)1 << 21), gx = ceil_div(blocks, gy);
   // Arrays of 128 MB or more are gone from the last-level cache before the next
   // operator reads them: past the caches, 16384 rows of 7168 bf16 with residual
-  // and both outputs take 185 instead of 192 us (5.7 TB/s), while at 8192 rows of
-  // 2048 (32 MB arrays) a forward and backward pass take 57 instead of 52 us.
+  // and both outputs take 181 instead of 192 us (5.8 TB/s), while at 8192 rows of
+  // 2048 (32 MB arrays) a forward and backward pass take 58 instead of 52 us.
   const bool nt = (double)p.T * p.d_model * (p.dtype == MOE_DTYPE_BF16 ? 2 : 4) >= (double)(128 << 20);
 #define MOE_NORM_LAUNCH(BF16, TPR, VPT, NT)                                                                      \
   hipLaunchKernelGGL((add_rmsnorm_kernel<BF16, TPR, VPT, NT>), dim3((unsigned)gx, (unsigned)gy),                 \
