@@ -237,7 +237,7 @@ moe_status_t moe_forward(const moe_problem_t* p, const void* x, const void* w_ro
  * GELU_tanh(U), the expert outputs). H is GELU_tanh of the bf16-rounded U,
  * so y can differ from moe_forward's (which rounds once, after GELU) in the
  * last bits. bf16 only, k <= 8, E a multiple of 8, x under 2 GiB;
- * otherwise MOE_ERR_UNSUPPORTED.
+ * otherwise MOE_ERR_UNSUPPORTED. (moe_backward has further limits of size.)
  *   ws at least moe_workspace_size(p, MOE_STAGE_TRAIN) bytes; the caller keeps
  *   it untouched until the matching moe_backward call has been enqueued */
 moe_status_t moe_forward_train(const moe_problem_t* p, const void* x, const void* w_router,

@@ -96,10 +96,11 @@ __device__ __forceinline__ void find_rows(const int32_t* __restrict__ offsets, i
 // Bound by the weights' bytes (8 tokens of 64 experts of 7168 x 2048, top-8: 210 us,
 // 5.5 TB/s), for few of them by the chain offsets, row numbers, rows, sums (one
 // token of 2048 x 1024 10 + 5 us: the first product's 128 columns, those of a scale
-// block, leave it 64 workgroups for 256 CUs, the second one has 256). 1, 2 or 4 waves along the contraction are within
-// 4% of each other at 1 to 777 tokens but for wide experts' second product (8192:
-// 1 wave 64 us, 4 waves 50); loading the next weights ahead in registers costs the
-// second workgroup of a CU (one token 13.5 -> 18.1 us).
+// block, leave it 64 workgroups for 256 CUs, the second one has 256). 1, 2 or 4
+// waves along the contraction are within 4% of each other at 1 to 777 tokens but for
+// wide experts' second product (8192: 1 wave 64 us, 4 waves 50); loading the next
+// weights ahead in registers costs the second workgroup of a CU (one token 13.5 ->
+// 18.1 us).
 template <int NG, int KS, bool ACT>
 __global__ __launch_bounds__(NG * KS * kWave) void gemm_fp8_small_kernel(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ As, const int32_t* __restrict__ perm, int64_t a_rows,
@@ -837,10 +838,10 @@ int64_t m_tiles_bound(int64_t R, int E, int bm) { return min(R, (R + (int64_t)E 
 // that read the weights straight into registers. The tiles do a matrix
 // instruction's work with an eighth of the weight reads, the small form has no
 // pipeline to fill and eight times the workgroups. Both estimates in us, from
-// times on MI355X over 1 .. 6000 tokens of five layer shapes (three below): a workgroup of the
-// small form costs about 0.7 us per block of 128 positions and 128 columns, four
-// blocks' worth of it before the first; a tile 1.5 us a block and 6 us around
-// them, per round of tiles. Both products of a layer, us, small form / tiles:
+// times on MI355X over 1 .. 6000 tokens of five layer shapes (three below): a
+// workgroup of the small form costs about 0.7 us per block of 128 positions and 128
+// columns, four blocks' worth of it before the first; a tile 1.5 us a block and 6 us
+// around them, per round of tiles. Both products of a layer, us, small form / tiles:
 // 8192-wide coarse experts at 8 rows an expert 50 / 102, at 128 220 / 125;
 // 64 fine experts of 2048 x 1024 at 4 rows 50 / 56, at 64 132 / 63; 12 experts of
 // 320 x 448 at 194 rows 17 / 26, at 1500 65 / 31. (Workgroups of 64 and 128 rows

@@ -21,7 +21,8 @@ def test_cases_cover_the_ways_to_cut():
     every = [c for cs in by.values() for c in cs]
     assert max(sum(1 for z in cs if z.xcd == c.xcd) for cs in by.values() for c in cs) >= 2  # several on one XCD
     assert any(p.slot == 1 for c in every for p in c.parts)            # a workgroup with parts of two tiles
-    assert any(len(c.parts) <= 4 for c in every) and any(len(c.parts) > 4 for c in every)  # one and more rounds of the join
+    # one and more rounds of the join
+    assert any(len(c.parts) <= 4 for c in every) and any(len(c.parts) > 4 for c in every)
     assert {c.rows for c in every} >= {fr.TILE, 1} and any(1 < c.rows < 128 for c in every)
     assert any(c.cols < fr.TILE for c in every) and any(c.cols == fr.TILE for c in every)
     # after whole rounds

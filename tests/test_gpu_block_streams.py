@@ -11,7 +11,7 @@ pytestmark = [pytest.mark.gpu, needs_gpu]
 
 BF = torch.bfloat16
 T, D, E, K, DE = 70, 320, 8, 2, 448
-DELAY = 20_000_000  # cycles of a kernel that only waits: milliseconds, far longer than a constructor takes
+DELAY = 500_000_000  # cycles of a kernel that only waits, 0.2 s: far longer than a constructor or a call takes
 
 
 @pytest.fixture(scope="module")
