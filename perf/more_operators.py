@@ -468,15 +468,15 @@ def _plan(s):
     if case["op"] == "linear":
         K, N, train = case["K"], case["N"], case["train"]
         p = moe.make_problem(T, K, 1, 1, N, torch.bfloat16)
-        act = {"none": moe.MOEX_ACT_NONE, "gelu": moe.MOEX_ACT_GELU, "silu": moe.MOEX_ACT_SILU,
-               "relu": moe.MOEX_ACT_RELU}[case["act"]]
+        act = {"none": moe.MOET_ACT_NONE, "gelu": moe.MOET_ACT_GELU, "silu": moe.MOET_ACT_SILU,
+               "relu": moe.MOET_ACT_RELU}[case["act"]]
         o = {"y": new((T, N), torch.bfloat16)}
-        ws = new((moe.moex_workspace_size(p, moe.MOEX_STAGE_LINEAR),), torch.uint8)
+        ws = new((moe.moet_workspace_size(p, moe.MOET_STAGE_LINEAR),), torch.uint8)
         if train:
             o.update(u=new((T, N), torch.bfloat16), dx=new((T, K), torch.bfloat16), dW=new((K, N), torch.bfloat16))
             if case["bias"]:
                 o["dbias"] = new((N,), torch.bfloat16)
-            ws = (ws, new((moe.moex_workspace_size(p, moe.MOEX_STAGE_LINEAR_BACKWARD),), torch.uint8))
+            ws = (ws, new((moe.moet_workspace_size(p, moe.MOET_STAGE_LINEAR_BACKWARD),), torch.uint8))
         s["plan"] = (moe, p, act, o, ws)
         return s["plan"]
     d, E, k, dt = case["d"], case["E"], case["k"], s["x"].dtype
@@ -486,7 +486,7 @@ def _plan(s):
     if case["train"]:
         o.update(dy_perm=new((T * k, d), dt), dx=new((T, d), dt), dgate=new((T, k), torch.float32),
                  dlogits=new((T, E), torch.float32))
-    ws = new((moe.moex_workspace_size(p, moe.MOEX_STAGE_DISPATCH),), torch.uint8)
+    ws = new((moe.moet_workspace_size(p, moe.MOET_STAGE_DISPATCH),), torch.uint8)
     s["plan"] = (moe, p, o, ws)
     return s["plan"]
 
@@ -502,22 +502,22 @@ def _own(s):
     if case["op"] == "linear":
         moe, p, act, o, ws = plan
         if not case["train"]:
-            moe.moex_linear(p, s["x"], s["W"], s["bias"], act, s["residual"], None, o["y"], ws)
+            moe.moet_linear(p, s["x"], s["W"], s["bias"], act, s["residual"], None, o["y"], ws)
         else:
-            moe.moex_linear(p, s["x"], s["W"], s["bias"], act, s["residual"], o["u"], o["y"], ws[0])
-            moe.moex_linear_backward(p, s["x"], s["W"], o["u"], act, s["dy"], o["dx"], o["dW"], o.get("dbias"), ws[1])
+            moe.moet_linear(p, s["x"], s["W"], s["bias"], act, s["residual"], o["u"], o["y"], ws[0])
+            moe.moet_linear_backward(p, s["x"], s["W"], o["u"], act, s["dy"], o["dx"], o["dW"], o.get("dbias"), ws[1])
         return dict(o)
     moe, p, o, ws = plan
     w_in, w_out = (s["gate"], None) if case["early"] else (None, s["gate"])
-    moe.moex_dispatch(p, s["idx"], w_in, s["x"], o["counts"], o["offsets"], o["perm"], o["inv"], o["x_perm"], ws)
-    moe.moex_combine(p, s["y_perm"], o["inv"], w_out, s["residual"], o["y"])
+    moe.moet_dispatch(p, s["idx"], w_in, s["x"], o["counts"], o["offsets"], o["perm"], o["inv"], o["x_perm"], ws)
+    moe.moet_combine(p, s["y_perm"], o["inv"], w_out, s["residual"], o["y"])
     if case["train"]:
         early = case["early"]
-        moe.moex_combine_backward(p, s["dy"], o["inv"], None if early else s["y_perm"], w_out, o["dy_perm"],
+        moe.moet_combine_backward(p, s["dy"], o["inv"], None if early else s["y_perm"], w_out, o["dy_perm"],
                                   None if early else o["dgate"])
-        moe.moex_dispatch_backward(p, s["dx_perm"], o["inv"], s["x"] if early else None, w_in, s["dh"], o["dx"],
+        moe.moet_dispatch_backward(p, s["dx_perm"], o["inv"], s["x"] if early else None, w_in, s["dh"], o["dx"],
                                    o["dgate"] if early else None)
-        moe.moex_gate_backward(p, s["logits"], s["idx"], o["dgate"], None, o["dlogits"])
+        moe.moet_gate_backward(p, s["logits"], s["idx"], o["dgate"], None, o["dlogits"])
     return dict(o)
 
 
