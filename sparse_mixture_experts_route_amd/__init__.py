@@ -1,7 +1,8 @@
 """MI355X (gfx950) sparse Mixture-of-Experts layer forward.
 
-Thin Python binding over libmoe.so's C ABI (include/moe.h, and include/moe_ext.h
-for the operators around the layer): the functions below carry the C names and only marshal arguments (torch tensors are device
+Thin Python binding over libmoe.so's C ABI (include/moe.h, include/moe_ext.h
+for the operators around the layer, include/moe_train.h for what trains its
+surroundings): the functions below carry the C names and only marshal arguments (torch tensors are device
 buffers; their data pointers and torch's current HIP stream go to the
 library). Every step of the layer runs in the library's HIP kernels; there is
 no CPU or PyTorch fallback, and importing fails when the library is missing.
@@ -53,4 +54,28 @@ from ._ext import (  # noqa: F401
     moex_workspace_size,
     scale_pitch,
 )
+from ._train import (  # noqa: F401
+    MOET_ACT_GELU,
+    MOET_ACT_NONE,
+    MOET_ACT_RELU,
+    MOET_ACT_SILU,
+    MOET_GRAD_NORM_WS_BYTES,
+    MOET_MAX_TENSORS,
+    MOET_STAGE_DISPATCH,
+    MOET_STAGE_LINEAR,
+    MOET_STAGE_LINEAR_BACKWARD,
+    AdamWOptions,
+    Tensor,
+    moet_adamw,
+    moet_combine,
+    moet_combine_backward,
+    moet_dispatch,
+    moet_dispatch_backward,
+    moet_gate_backward,
+    moet_grad_norm,
+    moet_workspace_size,
+    set_grad,
+    tensor_entry,
+)
 from .layer import MoEBlockFP8, MoEForward  # noqa: F401
+from .optim import AdamW  # noqa: F401

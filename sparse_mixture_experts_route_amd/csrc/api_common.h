@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "internal.h"
 
 #define MOE_API extern "C" __attribute__((visibility("default")))
@@ -26,6 +28,33 @@ inline moe_status_t check_problem(const moe_problem_t* p) {
   if (p->T > (int64_t)INT32_MAX / p->k) return MOE_ERR_UNSUPPORTED;
   if (p->d_model % 64 != 0 || p->d_expert % 64 != 0) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
+}
+
+// A caller's buffer: NULL means it was left out.
+struct Buf {
+  const void* ptr;
+  size_t bytes;
+  bool out;
+};
+
+inline Buf in(const void* p, size_t n) { return {p, n, false}; }
+inline Buf out(const void* p, size_t n) { return {p, n, true}; }
+
+// Alignment of every buffer, and no output overlapping another buffer.
+inline bool buffers_ok(std::initializer_list<Buf> bufs) {
+  for (const Buf& a : bufs) {
+    if (!a.ptr) continue;
+    if (!aligned16(a.ptr)) return false;
+    const uintptr_t a0 = (uintptr_t)a.ptr;
+    if (a.bytes > UINTPTR_MAX - a0) return false;
+    if (!a.out) continue;
+    for (const Buf& b : bufs) {
+      if (&a == &b || !b.ptr) continue;
+      const uintptr_t b0 = (uintptr_t)b.ptr;
+      if (a0 < b0 + b.bytes && b0 < a0 + a.bytes) return false;
+    }
+  }
+  return true;
 }
 
 // Sequential sub-allocation of a caller-provided workspace (or size counting when base is null).

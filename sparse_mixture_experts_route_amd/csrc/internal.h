@@ -45,11 +45,12 @@ hipError_t launch_finalize_permute_small(const moe_problem_t& p, const float* pa
                                         int nzero = 0);
 
 // counts/offsets/perm/inv from the routing table; blockcounts/blockbase are
-// workspace arrays of permute_blocks(T) * E int32 each.
+// workspace arrays of permute_blocks(T) * E int32 each. repeats: a token may name
+// an expert twice (each gets a row; forms 1 and 2 alone).
 hipError_t launch_permute_index(const moe_problem_t& p, const int32_t* idx, int32_t* counts,
                                 int32_t* offsets, int32_t* perm, int32_t* inv,
                                 int32_t* blockcounts, int32_t* blockbase, hipStream_t s, int32_t* zero = nullptr,
-                                int nzero = 0);
+                                int nzero = 0, bool repeats = false);
 
 // Form of launch_permute_index for p: 0 one workgroup (T <= kSmallPermuteT,
 // k <= 8), 1 per-block histograms then a scatter that scans for itself,
@@ -190,5 +191,20 @@ hipError_t launch_gemm_fp8(const void* A, const void* As, const int32_t* perm, i
                            float* partials, hipStream_t s);
 // Float32 partial-sum bytes of a product without activation (0: none are used)
 size_t gemm_fp8_partials_bytes(int64_t R, int K, int N, int E);
+
+// ---- rows sorted by expert and back (moe_train.h)
+// One launch for a few selections: index and rows together.
+bool dispatch_small(const moe_problem_t& p);
+hipError_t launch_dispatch_small(const moe_problem_t& p, const int32_t* idx, const float* w, const void* x,
+                                 int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv, void* x_perm,
+                                 hipStream_t s);
+// dst[inv[t, j]] = w[t, j] src[t], and with dw its dot product with rows[inv[t, j]]; w may be null
+hipError_t launch_to_rows(const moe_problem_t& p, const void* src, const int32_t* inv, const float* w, const void* rows,
+                          void* dst, float* dw, hipStream_t s);
+// dst[t] = add[t] + sum over j of w[t, j] rows[inv[t, j]], and with dw their dot products with x[t]; w, add may be null
+hipError_t launch_from_rows(const moe_problem_t& p, const void* rows, const int32_t* inv, const float* w, const void* add,
+                            const void* x, void* dst, float* dw, hipStream_t s);
+hipError_t launch_gate_backward(const moe_problem_t& p, const float* logits, const int32_t* idx, const float* dgate,
+                                const float* add, float* dlogits, hipStream_t s);
 
 }  // namespace moe

@@ -5,7 +5,6 @@
 #include <stdint.h>
 
 #include <cmath>
-#include <initializer_list>
 
 #include "../../include/moe_ext.h"
 #include "api_common.h"
@@ -14,33 +13,6 @@
 using namespace moe;
 
 namespace {
-
-// A caller's buffer: NULL means it was left out.
-struct Buf {
-  const void* ptr;
-  size_t bytes;
-  bool out;
-};
-
-inline Buf in(const void* p, size_t n) { return {p, n, false}; }
-inline Buf out(const void* p, size_t n) { return {p, n, true}; }
-
-// Alignment of every buffer, and no output overlapping another buffer.
-bool buffers_ok(std::initializer_list<Buf> bufs) {
-  for (const Buf& a : bufs) {
-    if (!a.ptr) continue;
-    if (!aligned16(a.ptr)) return false;
-    const uintptr_t a0 = (uintptr_t)a.ptr;
-    if (a.bytes > UINTPTR_MAX - a0) return false;
-    if (!a.out) continue;
-    for (const Buf& b : bufs) {
-      if (&a == &b || !b.ptr) continue;
-      const uintptr_t b0 = (uintptr_t)b.ptr;
-      if (a0 < b0 + b.bytes && b0 < a0 + a.bytes) return false;
-    }
-  }
-  return true;
-}
 
 // The gradient's factor coef E has to stay finite: masked rows multiply it by 0.
 bool coef_ok(const moe_problem_t& p, float coef) { return std::isfinite(coef * (float)p.E); }

@@ -1,0 +1,347 @@
+// AdamW over a list of tensors, moments in 32 or 8 bits, and the gradients' norm.
+//
+//   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2
+//   p -= lr (m / (1 - b1^t) / (sqrt(v / (1 - b2^t)) + eps) + decay p)
+//
+// Every value is read and written once: HBM is the bound (28 bytes a value for
+// bfloat16 parameters with a master copy and moments in 32 bits, 16 with moments
+// in 8). A thread has 8 consecutive values, so 16 neighbouring lanes (a DPP row)
+// have the 128 that share a scale. Workgroups take chunks of the whole list in
+// turn; the list is in the kernel's arguments.
+//
+// The moments are updated in 64 bits, where a CU multiplies as fast as in
+// 32: their codes then do not depend on how the two products are rounded.
+#include "common.h"
+#include "e4m3.h"
+#include "optim.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kVals = 8;
+
+__device__ __forceinline__ uint32_t mix32(uint32_t x) {
+  x ^= x >> 16;
+  x *= 0x7FEB352Du;
+  x ^= x >> 15;
+  x *= 0x846CA68Bu;
+  return x ^ (x >> 16);
+}
+
+// 8 values of a float32 or bfloat16 array from value i0 on; those at or past n are 0
+template <bool B16>
+__device__ __forceinline__ void load_vals(const void* base, int64_t i0, int64_t n, bool whole, float* f) {
+  if (whole) {
+    if constexpr (B16) {
+      const u32x4 q = *(const u32x4*)((const bf16_bits*)base + i0);
+#pragma unroll
+      for (int i = 0; i < kVals; ++i)
+        f[i] = (i & 1) ? __uint_as_float(q[i / 2] & 0xFFFF0000u) : __uint_as_float(q[i / 2] << 16);
+    } else {
+      const f32x4* p = (const f32x4*)((const float*)base + i0);
+      const f32x4 a = p[0], b = p[1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[i] = a[i];
+        f[4 + i] = b[i];
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kVals; ++i) {
+    f[i] = 0.0f;
+    if (i0 + i < n) f[i] = B16 ? bf16_to_f32(((const bf16_bits*)base)[i0 + i]) : ((const float*)base)[i0 + i];
+  }
+}
+
+template <bool B16>
+__device__ __forceinline__ void store_vals(void* base, int64_t i0, int64_t n, bool whole, const float* f) {
+  if (whole) {
+    if constexpr (B16) {
+      u32x4 q;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+      *(u32x4*)((bf16_bits*)base + i0) = q;
+    } else {
+      f32x4* p = (f32x4*)((float*)base + i0);
+      p[0] = f32x4{f[0], f[1], f[2], f[3]};
+      p[1] = f32x4{f[4], f[5], f[6], f[7]};
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kVals; ++i) {
+    if (i0 + i >= n) continue;
+    if constexpr (B16) ((bf16_bits*)base)[i0 + i] = (bf16_bits)(pack_bf16x2(f[i], 0.0f) & 0xFFFFu);
+    else ((float*)base)[i0 + i] = f[i];
+  }
+}
+
+// 8 bytes of codes from i0 on
+__device__ __forceinline__ u32x2 load_codes(const void* base, int64_t i0, int64_t n, bool whole) {
+  const uint8_t* p = (const uint8_t*)base + i0;
+  if (whole) return *(const u32x2*)p;
+  u32x2 q = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < kVals; ++i)
+    if (i0 + i < n) q[i / 4] |= (uint32_t)p[i] << (8 * (i % 4));
+  return q;
+}
+
+__device__ __forceinline__ void store_codes(void* base, int64_t i0, int64_t n, bool whole, const u32x2& q) {
+  uint8_t* p = (uint8_t*)base + i0;
+  if (whole) {
+    *(u32x2*)p = q;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kVals; ++i)
+    if (i0 + i < n) p[i] = (uint8_t)(q[i / 4] >> (8 * (i % 4)));
+}
+
+// e4m3 (E5 false) or e5m2 codes as float32 values
+template <bool E5>
+__device__ __forceinline__ void decode8(const u32x2& q, float* f) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const f32x2 a = E5 ? __builtin_amdgcn_cvt_pk_f32_bf8(q[i], false) : __builtin_amdgcn_cvt_pk_f32_fp8(q[i], false);
+    const f32x2 b = E5 ? __builtin_amdgcn_cvt_pk_f32_bf8(q[i], true) : __builtin_amdgcn_cvt_pk_f32_fp8(q[i], true);
+    f[4 * i] = a[0];
+    f[4 * i + 1] = a[1];
+    f[4 * i + 2] = b[0];
+    f[4 * i + 3] = b[1];
+  }
+}
+
+// 2^e in 64 bits
+__device__ __forceinline__ double pow2(int e) { return __longlong_as_double((long long)(1023 + e) << 52); }
+
+// The smallest float32 that is not below |x|
+__device__ __forceinline__ float up32(double x) {
+  const float f = (float)fabs(x);
+  return (double)f < fabs(x) && f < INFINITY ? __uint_as_float(__float_as_uint(f) + 1u) : f;
+}
+
+// A scaled value to its code with random number r < 2^16: e4m3 (3 bits of
+// mantissa, bias 7) or e5m2 (2 bits, bias 15). The spacing at a normal value is
+// its exponent's, so floor(|x| / s + r / 2^16) is an addition to the bits below
+// the mantissa kept: those in the upper half of the double are enough, as r ends
+// above the others. Subnormal codes count units of the smallest spacing.
+template <bool E5>
+__device__ __forceinline__ uint32_t encode(double x, uint32_t r) {
+  constexpr int M = E5 ? 2 : 3, BIAS = E5 ? 15 : 7, CUT = 20 - M;
+  const double a = fabs(x);
+  const uint32_t hi = (uint32_t)__double2hiint(x) & 0x7FFFFFFFu;
+  uint32_t c = ((hi + (r << (CUT - 16))) >> CUT) - ((uint32_t)(1023 - BIAS) << M);
+  if (a < pow2(1 - BIAS)) c = ((uint32_t)(a * pow2(BIAS - 1 + M + 16)) + r) >> 16;
+  if (E5 && c == 0u && a > 0.0) c = 1u;  // a second moment that is not 0
+  if (!(a <= (E5 ? 57344.0 : 448.0))) c = 0x7Fu;
+  return E5 ? c : c | (((uint32_t)__double2hiint(x) >> 24) & 0x80u);
+}
+
+struct Hyper {
+  double b1, b2, gs;
+  float step, root, lr, eps;  // lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
+  uint32_t key;
+};
+
+template <bool G16, bool P16, bool S8>
+__device__ __forceinline__ void update(const OptTensor& T, const Hyper& h, int64_t i0) {
+  const int64_t n = T.n;
+  const bool whole = i0 + kVals <= n;
+  float g[kVals], p[kVals], mf[kVals], vf[kVals];
+  double m[kVals], v[kVals];
+  load_vals<G16>(T.grad, i0, n, whole, g);
+  load_vals<false>(P16 ? T.master : (const float*)T.param, i0, n, whole, p);
+  const int64_t block = i0 / kQBlock;
+  const bool inside = i0 < n;
+  if constexpr (S8) {
+    const u32x2 mq = load_codes(T.m, i0, n, whole), vq = load_codes(T.v, i0, n, whole);
+    const double ms = pow2(inside ? (int)T.m_scale[block] - 127 : 0), vs = pow2(inside ? (int)T.v_scale[block] - 127 : 0);
+    decode8<false>(mq, mf);
+    decode8<true>(vq, vf);
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) {
+      m[i] = (double)mf[i] * ms;
+      v[i] = (double)vf[i] * vs;
+    }
+  } else {
+    load_vals<false>(T.m, i0, n, whole, mf);
+    load_vals<false>(T.v, i0, n, whole, vf);
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) {
+      m[i] = mf[i];
+      v[i] = vf[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kVals; ++i) {
+    const double d = (double)g[i] * h.gs;
+    // products and sums rounded one by one: the same bits wherever they are computed
+    m[i] = __dadd_rn(__dmul_rn(h.b1, m[i]), __dmul_rn(1.0 - h.b1, d));
+    v[i] = __dadd_rn(__dmul_rn(h.b2, v[i]), __dmul_rn(__dmul_rn(1.0 - h.b2, d), d));
+    mf[i] = (float)m[i];
+    vf[i] = (float)v[i];
+    const float move = h.step * mf[i] / (sqrtf(vf[i]) * h.root + h.eps);
+    p[i] = p[i] - fmaf(h.lr * T.weight_decay, p[i], move);
+  }
+  store_vals<false>(P16 ? (void*)T.master : T.param, i0, n, whole, p);
+  if constexpr (P16) store_vals<true>(T.param, i0, n, whole, p);
+  if constexpr (S8) {
+    float mt = 0.0f, vt = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) {
+      if (i0 + i < n) {
+        mt = fmaxf(mt, up32(m[i]));
+        vt = fmaxf(vt, up32(v[i]));
+      }
+    }
+    // the lanes of a DPP row have the 128 values of a scale; 57344 is 1.75 2^15, 448 is 1.75 2^8
+    const int mb = scale_byte(row16_max(mt));
+    const uint32_t vu = __float_as_uint(row16_max(vt));
+    const int vb = min(max((int)((vu + 0x1FFFFFu) >> 23) - 142, -120), 120) + 127;
+    const double mi = pow2(127 - mb), vi = pow2(127 - vb);
+    u32x2 mq = {0u, 0u}, vq = {0u, 0u};
+    const uint32_t high = (uint32_t)((uint64_t)i0 >> 32) * 0x9E3779B9u;  // a chunk does not cross 2^32
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) {
+      const uint32_t r = mix32(((uint32_t)(i0 + i) + h.key) ^ high);
+      mq[i / 4] |= encode<false>(m[i] * mi, r & 0xFFFFu) << (8 * (i % 4));
+      vq[i / 4] |= encode<true>(v[i] * vi, r >> 16) << (8 * (i % 4));
+    }
+    store_codes(T.m, i0, n, whole, mq);
+    store_codes(T.v, i0, n, whole, vq);
+    if (inside && i0 % kQBlock == 0) {
+      T.m_scale[block] = (uint8_t)mb;
+      T.v_scale[block] = (uint8_t)vb;
+    }
+  } else {
+    store_vals<false>(T.m, i0, n, whole, mf);
+    store_vals<false>(T.v, i0, n, whole, vf);
+  }
+}
+
+// Index of the tensor that chunk c is of: the last whose first chunk is not above it
+template <typename L>
+__device__ __forceinline__ int tensor_of(const L& l, int c) {
+  int a = 0, b = l.count;
+  while (b - a > 1) {
+    const int mid = (a + b) >> 1;
+    if (l.t[mid].first <= c) a = mid;
+    else b = mid;
+  }
+  return a;
+}
+
+__global__ __launch_bounds__(kOptThreads) void adamw_kernel(const OptList l, const OptHyper o,
+                                                            int32_t* __restrict__ counter,
+                                                            const float* __restrict__ lr_scale,
+                                                            const float* __restrict__ grad_scale) {
+  const int32_t before = __hip_atomic_load(counter, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const float gs = grad_scale ? *grad_scale : 1.0f;
+  const bool skip = gs != gs;
+  if (!skip) {
+    const double t = (double)(before + 1);
+    const double c1 = -expm1(t * o.log_beta1), c2 = -expm1(t * o.log_beta2);
+    const double lr = o.lr * (lr_scale ? (double)*lr_scale : 1.0);
+    const uint32_t draw = (uint32_t)(before + 1) * 0x9E3779B9u;
+    for (int c = blockIdx.x; c < l.chunks; c += gridDim.x) {
+      const int j = tensor_of(l, c);
+      const OptTensor& T = l.t[j];
+      const double f = lr * (double)T.lr_factor;
+      Hyper h;
+      h.b1 = o.beta1;
+      h.b2 = o.beta2;
+      h.gs = gs;
+      h.step = (float)(f / c1);
+      h.root = (float)(1.0 / sqrt(c2));
+      h.lr = (float)f;
+      h.eps = o.eps;
+      h.key = mix32(o.seed + mix32(draw + (uint32_t)(l.base + j)));
+      const int64_t i0 = (int64_t)(c - T.first) * kOptChunk + threadIdx.x * kVals;
+      switch (T.flags) {  // the same for the whole workgroup
+        case 0: update<false, false, false>(T, h, i0); break;
+        case kGrad16: update<true, false, false>(T, h, i0); break;
+        case kParam16: update<false, true, false>(T, h, i0); break;
+        case kGrad16 | kParam16: update<true, true, false>(T, h, i0); break;
+        case kMoments8: update<false, false, true>(T, h, i0); break;
+        case kGrad16 | kMoments8: update<true, false, true>(T, h, i0); break;
+        case kParam16 | kMoments8: update<false, true, true>(T, h, i0); break;
+        default: update<true, true, true>(T, h, i0); break;
+      }
+    }
+  }
+  if (!l.last) return;
+  // The last workgroup to come here advances the counter: all have read it by then,
+  // this one's other waves included.
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const int32_t n = __hip_atomic_fetch_add(counter + 1, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    if (n == (int32_t)gridDim.x - 1) {
+      __hip_atomic_store(counter + 1, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (!skip) __hip_atomic_store(counter, before + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+  }
+}
+
+// Sum of 256 threads' values, the same order every time; thread 0 has it
+__device__ __forceinline__ double block_sum(double v, double* slots) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
+  if (threadIdx.x % kWave == 0) slots[threadIdx.x / kWave] = v;
+  __syncthreads();
+  return threadIdx.x == 0 ? (slots[0] + slots[1]) + (slots[2] + slots[3]) : 0.0;
+}
+
+__global__ __launch_bounds__(kOptThreads) void square_sums_kernel(const NormList l, double* __restrict__ slots) {
+  __shared__ double s_v[kOptThreads / kWave];
+  double sum = 0.0;
+  for (int c = blockIdx.x; c < l.chunks; c += gridDim.x) {
+    const NormTensor& T = l.t[tensor_of(l, c)];
+    const int64_t i0 = (int64_t)(c - T.first) * kOptChunk + threadIdx.x * kVals;
+    float g[kVals];
+    if (T.flags) load_vals<true>(T.grad, i0, T.n, i0 + kVals <= T.n, g);
+    else load_vals<false>(T.grad, i0, T.n, i0 + kVals <= T.n, g);
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) sum = fma((double)g[i], (double)g[i], sum);
+  }
+  sum = block_sum(sum, s_v);
+  if (threadIdx.x == 0) slots[blockIdx.x] = l.add ? slots[blockIdx.x] + sum : sum;
+}
+
+__global__ __launch_bounds__(kOptThreads) void norm_scale_kernel(const double* __restrict__ slots, double max_norm,
+                                                                 float* __restrict__ norm, float* __restrict__ scale) {
+  __shared__ double s_v[kOptThreads / kWave];
+  double v = 0.0;
+#pragma unroll
+  for (int i = 0; i < kNormSlots / kOptThreads; ++i) v += slots[i * kOptThreads + threadIdx.x];
+  v = block_sum(v, s_v);
+  if (threadIdx.x == 0) {
+    const double n = sqrt(v);
+    norm[0] = (float)n;
+    if (scale) scale[0] = n <= max_norm ? 1.0f : n < INFINITY ? (float)(max_norm / n) : NAN;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_adamw(const OptList& l, const OptHyper& h, int32_t* counter, const float* lr_scale,
+                        const float* grad_scale, hipStream_t s) {
+  const unsigned grid = (unsigned)max(1, min(l.chunks, 2048));
+  hipLaunchKernelGGL(adamw_kernel, dim3(grid), dim3(kOptThreads), 0, s, l, h, counter, lr_scale, grad_scale);
+  return hipGetLastError();
+}
+
+hipError_t launch_square_sums(const NormList& l, double* slots, hipStream_t s) {
+  hipLaunchKernelGGL(square_sums_kernel, dim3(kNormSlots), dim3(kOptThreads), 0, s, l, slots);
+  return hipGetLastError();
+}
+
+hipError_t launch_norm_scale(const double* slots, double max_norm, float* norm, float* scale, hipStream_t s) {
+  hipLaunchKernelGGL(norm_scale_kernel, dim3(1), dim3(kOptThreads), 0, s, slots, max_norm, norm, scale);
+  return hipGetLastError();
+}
+
+}  // namespace moe

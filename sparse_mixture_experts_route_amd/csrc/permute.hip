@@ -38,31 +38,46 @@ namespace {
 constexpr int kTB = kPermuteTokensPerBlock;  // tokens per block, one thread each
 constexpr int kWords = kTB / 32;             // mask words per expert
 
-__device__ __forceinline__ void build_mask(const int32_t* __restrict__ idx, int64_t T, int k, int E,
-                                           uint32_t (*mask)[kWords], int64_t t0) {
+// REPEATS: a token may name an expert twice. `extra[e]` then counts the selections
+// that a mask has no bit for, and the result says whether the block has any.
+template <bool REPEATS = false>
+__device__ __forceinline__ bool build_mask(const int32_t* __restrict__ idx, int64_t T, int k, int E,
+                                           uint32_t (*mask)[kWords], int64_t t0, int* extra = nullptr) {
   uint32_t* flat = &mask[0][0];
   for (int i = threadIdx.x; i < E * kWords; i += kTB) flat[i] = 0u;
+  if (REPEATS && (int)threadIdx.x < E) extra[threadIdx.x] = 0;
   __syncthreads();
   const int64_t t = t0 + threadIdx.x;
+  bool again = false;
   if (t < T) {
     for (int j = 0; j < k; ++j) {
       const int e = idx[t * k + j];
-      if ((unsigned)e < (unsigned)E) atomicOr(&mask[e][threadIdx.x >> 5], 1u << (threadIdx.x & 31));
+      if ((unsigned)e < (unsigned)E) {
+        const uint32_t bit = 1u << (threadIdx.x & 31);
+        if (atomicOr(&mask[e][threadIdx.x >> 5], bit) & bit) {
+          again = true;
+          if (REPEATS) atomicAdd(&extra[e], 1);
+        }
+      }
     }
   }
+  if (REPEATS) return __syncthreads_or(again);
   __syncthreads();
+  return false;
 }
 
+template <bool REPEATS>
 __global__ __launch_bounds__(kTB) void hist_kernel(const int32_t* __restrict__ idx, int64_t T, int k, int E,
                                                    int32_t* __restrict__ blockcounts, int32_t* __restrict__ zero,
                                                    int nzero) {
   __shared__ uint32_t mask[256][kWords];
+  __shared__ int extra[REPEATS ? 256 : 1];
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < nzero; i += kTB) zero[i] = 0;
-  build_mask(idx, T, k, E, mask, (int64_t)blockIdx.x * kTB);
+  build_mask<REPEATS>(idx, T, k, E, mask, (int64_t)blockIdx.x * kTB, extra);
   const int e = threadIdx.x;
   if (e < E) {
-    int c = 0;
+    int c = REPEATS ? extra[e] : 0;
 #pragma unroll
     for (int w = 0; w < kWords; ++w) c += __popc(mask[e][w]);
     blockcounts[(int64_t)blockIdx.x * E + e] = c;
@@ -167,13 +182,16 @@ constexpr int kFusedScanBlocks = 64;
 // every block sums them per expert (in total and over the blocks before it),
 // scans the totals over the experts, and block 0 writes counts and offsets.
 // Otherwise `blockcounts` is scan_kernel's first row of every (block, expert).
-template <bool SCAN>
+// REPEATS: where a token of the block names an expert twice, ranks are counted
+// over the block's selections instead of read from the masks.
+template <bool SCAN, bool REPEATS>
 __global__ __launch_bounds__(kTB) void scatter_kernel(const int32_t* __restrict__ idx, int64_t T, int k, int E,
                                                       const int32_t* __restrict__ blockcounts, int64_t nb,
                                                       int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
                                                       int32_t* __restrict__ perm, int32_t* __restrict__ inv) {
   __shared__ uint32_t mask[256][kWords];
   __shared__ int32_t s_base[256];
+  __shared__ int extra[REPEATS ? 256 : 1];
   const int64_t t0 = (int64_t)blockIdx.x * kTB;
   const int e0 = threadIdx.x;  // kTB = 256 threads: one expert slot each
   if constexpr (SCAN) {
@@ -210,9 +228,22 @@ __global__ __launch_bounds__(kTB) void scatter_kernel(const int32_t* __restrict_
     if (e0 < E) s_base[e0] = blockcounts[(int64_t)blockIdx.x * E + e0];
   }
   // this block's first row per expert is visible after build_mask's barriers
-  build_mask(idx, T, k, E, mask, t0);
+  const bool repeated = build_mask<REPEATS>(idx, T, k, E, mask, t0, extra);
   const int64_t t = t0 + threadIdx.x;
   if (t >= T) return;
+  if (REPEATS && repeated) {
+    for (int j = 0; j < k; ++j) {
+      const int e = idx[t * k + j];
+      int32_t r = -1;
+      if ((unsigned)e < (unsigned)E) {
+        r = s_base[e];
+        for (int64_t i = t0 * k; i < t * k + j; ++i) r += idx[i] == e;
+        perm[r] = (int32_t)t;
+      }
+      inv[t * k + j] = r;
+    }
+    return;
+  }
   const int w = threadIdx.x >> 5;
   const uint32_t below = (1u << (threadIdx.x & 31)) - 1u;
   // the selections in groups of 8, whose indices are loaded together
@@ -395,31 +426,31 @@ int permute_form(const moe_problem_t& p) {
 
 hipError_t launch_permute_index(const moe_problem_t& p, const int32_t* idx, int32_t* counts, int32_t* offsets,
                                 int32_t* perm, int32_t* inv, int32_t* blockcounts, int32_t* blockbase,
-                                hipStream_t s, int32_t* zero, int nzero) {
+                                hipStream_t s, int32_t* zero, int nzero, bool repeats) {
   if (!zero) nzero = 0;
   if (nzero < 0 || nzero > kSmallThreads) return hipErrorInvalidValue;
-  const int form = permute_form(p);
+  const int form = repeats ? permute_blocks(p.T) <= kFusedScanBlocks ? 1 : 2 : permute_form(p);
   if (form == 0) {
     hipLaunchKernelGGL(permute_small_kernel<false>, dim3(1), dim3(kSmallThreads), 0, s, idx, nullptr, 0, nullptr,
                        nullptr, nullptr, (int)p.T, p.k, p.E, counts, offsets, perm, inv, zero, nzero);
     return hipGetLastError();
   }
   const int64_t nb = permute_blocks(p.T);
-  hipLaunchKernelGGL(hist_kernel, dim3((unsigned)nb), dim3(kTB), 0, s, idx, p.T, p.k, p.E, blockcounts, zero,
-                     nzero);
+  hipLaunchKernelGGL(repeats ? hist_kernel<true> : hist_kernel<false>, dim3((unsigned)nb), dim3(kTB), 0, s, idx, p.T, p.k,
+                     p.E, blockcounts, zero, nzero);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   if (form == 1) {
-    hipLaunchKernelGGL(scatter_kernel<true>, dim3((unsigned)nb), dim3(kTB), 0, s, idx, p.T, p.k, p.E, blockcounts,
-                       nb, counts, offsets, perm, inv);
+    hipLaunchKernelGGL((repeats ? scatter_kernel<true, true> : scatter_kernel<true, false>), dim3((unsigned)nb), dim3(kTB),
+                       0, s, idx, p.T, p.k, p.E, blockcounts, nb, counts, offsets, perm, inv);
     return hipGetLastError();
   }
   hipLaunchKernelGGL(scan_kernel, dim3(1), dim3(kScanThreads), 0, s, blockcounts, nb, p.E, counts, offsets,
                      blockbase);
   err = hipGetLastError();
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(scatter_kernel<false>, dim3((unsigned)nb), dim3(kTB), 0, s, idx, p.T, p.k, p.E, blockbase, nb,
-                     counts, offsets, perm, inv);
+  hipLaunchKernelGGL((repeats ? scatter_kernel<false, true> : scatter_kernel<false, false>), dim3((unsigned)nb), dim3(kTB),
+                     0, s, idx, p.T, p.k, p.E, blockbase, nb, counts, offsets, perm, inv);
   return hipGetLastError();
 }
 

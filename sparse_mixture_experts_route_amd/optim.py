@@ -1,0 +1,106 @@
+"""AdamW over a list of tensors, on the library's moet_grad_norm and moet_adamw."""
+
+from __future__ import annotations
+
+from typing import Optional, Sequence
+
+import torch
+
+from . import _ext, _train
+
+_KINDS = ("master", "m", "m_scale", "v", "v_scale")
+
+
+class AdamW:
+    """The optimizer's state for a fixed list of parameters, and its step.
+
+    Parameters are float32, or bfloat16 with a float32 master copy that this object
+    holds. Moments are float32, or with bits=8 codes of 8 bits with a scale per 128
+    values (tensors of fewer than `least` values keep 32 bits; bits may also be one
+    number per parameter). lr_factor and weight_decay may be numbers or one per
+    parameter. With max_norm the gradients are clipped to that norm, and a step
+    whose gradients are not finite is left out altogether.
+
+    A step only enqueues work: it can be captured into a graph. It reads lr when it
+    is enqueued, and at every replay `lr_scale`, a float32 tensor of this object
+    that a schedule may write; the number of steps is kept on the GPU (`counter`).
+
+    state: buffers to go on from, lists by the names master, m, m_scale, v, v_scale
+    (None where a parameter has none) and counter, as `state` gives them; they are
+    used in place. All calls of an object are on one stream, or ordered by the caller.
+    """
+
+    def __init__(self, params: Sequence[torch.Tensor], lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
+                 weight_decay=0.01, lr_factor=1.0, bits=32, least: int = 4096, max_norm: Optional[float] = None,
+                 seed: int = 0, state: Optional[dict] = None):
+        self.params = list(params)
+        if not 1 <= len(self.params) <= _train.MOET_MAX_TENSORS:
+            raise ValueError(f"{len(self.params)} parameters, expected 1 to {_train.MOET_MAX_TENSORS}")
+        n = len(self.params)
+        self.device = torch.device("cuda", _ext._device("param", self.params[0]))
+        self.lr, self.betas, self.eps, self.seed, self.max_norm = lr, tuple(betas), eps, int(seed), max_norm
+        if max_norm is not None and not max_norm > 0:
+            raise ValueError("max_norm must be positive")
+
+        def each(v, name):
+            v = list(v) if isinstance(v, (list, tuple)) else [v] * n
+            if len(v) != n:
+                raise ValueError(f"{len(v)} values of {name} for {n} parameters")
+            return v
+
+        given = isinstance(bits, (list, tuple))
+        width = [b if given or p.numel() >= least else 32 for b, p in zip(each(bits, "bits"), self.params)]
+        if any(b not in (8, 32) for b in width):
+            raise ValueError("moments are held in 8 or in 32 bits")
+        if state is None:
+            state = self._fresh(width)
+        missing = [k for k in (*_KINDS, "counter") if k not in state]
+        if missing or any(len(state[k]) != n for k in _KINDS):
+            raise ValueError(f"state needs lists of {n} for {', '.join(_KINDS)}, and a counter")
+        for k in _KINDS:
+            setattr(self, k, list(state[k]))
+        self.counter = state["counter"]
+        self._list = (_train.Tensor * n)()
+        for i, (d, f) in enumerate(zip(each(weight_decay, "weight_decay"), each(lr_factor, "lr_factor"))):
+            if self.params[i].get_device() != self.device.index:
+                raise ValueError(f"parameter {i} is on {self.params[i].device}, the first on {self.device}")
+            self._list[i] = _train.tensor_entry(self.params[i], None, self.master[i], self.m[i], self.m_scale[i],
+                                                self.v[i], self.v_scale[i], float(f), float(d))
+        with torch.cuda.device(self.device):
+            self.lr_scale = torch.ones(1, device=self.device)
+            self.norm, self.scale = (torch.ones(1, device=self.device) for _ in range(2))
+            self._ws = torch.empty(_train.MOET_GRAD_NORM_WS_BYTES, dtype=torch.uint8, device=self.device)
+
+    def _fresh(self, width):
+        s = {k: [] for k in _KINDS}
+        for p, b in zip(self.params, width):
+            s["master"].append(p.detach().float().reshape(-1).contiguous() if p.dtype == torch.bfloat16 else None)
+            shape = (p.numel(),)
+            for k, t in (("m", torch.float8_e4m3fn), ("v", torch.float8_e5m2)):
+                codes = torch.zeros(shape, dtype=torch.uint8 if b == 8 else torch.float32, device=p.device)
+                s[k].append(codes.view(t) if b == 8 else codes)
+                # scales of zeros are the smallest, 2^-120
+                s[k + "_scale"].append(torch.full(((p.numel() + 127) // 128,), 7, dtype=torch.uint8, device=p.device)
+                                       if b == 8 else None)
+        s["counter"] = torch.zeros(2, dtype=torch.int32, device=self.device)
+        return s
+
+    @property
+    def state(self) -> dict:
+        """The buffers themselves (clone them to keep them)."""
+        return {**{k: list(getattr(self, k)) for k in _KINDS}, "counter": self.counter}
+
+    def step(self, grads: Sequence[torch.Tensor], stream=None) -> Optional[torch.Tensor]:
+        """One step with a gradient of each parameter, bfloat16 or float32. Returns the norm of the
+        gradients before clipping (this object's buffer), None without max_norm."""
+        if len(grads) != len(self.params):
+            raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
+        dev = self.device.index
+        for e, g in zip(self._list, grads):
+            _train.set_grad(e, g, dev)
+        opt = _train.AdamWOptions(self.lr, self.betas[0], self.betas[1], self.eps, self.seed & 0xFFFFFFFF)
+        if self.max_norm is not None:
+            _train.moet_grad_norm(self._list, self.max_norm, self.norm, self.scale, self._ws, stream)
+        _train.moet_adamw(self._list, opt, self.counter, self.lr_scale, self.scale if self.max_norm is not None else None,
+                          stream)
+        return self.norm if self.max_norm is not None else None
