@@ -73,6 +73,8 @@ from ._train import (  # noqa: F401
     moet_dispatch_backward,
     moet_gate_backward,
     moet_grad_norm,
+    moet_linear,
+    moet_linear_backward,
     moet_workspace_size,
     set_grad,
     tensor_entry,

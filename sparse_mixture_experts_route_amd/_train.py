@@ -55,6 +55,8 @@ def _declare():
         "moet_combine": [P, vp, vp, vp, vp, vp, vp],
         "moet_combine_backward": [P, vp, vp, vp, vp, vp, vp, vp],
         "moet_gate_backward": [P, vp, vp, vp, vp, vp, vp],
+        "moet_linear": [P, vp, vp, vp, i32, vp, vp, vp, vp, sz, vp],
+        "moet_linear_backward": [P, vp, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp],
         "moet_adamw": [A, i32, O, vp, vp, vp, vp],
         "moet_grad_norm": [A, i32, f64, vp, vp, vp, sz, vp],
     }
@@ -115,6 +117,23 @@ def moet_gate_backward(p: Problem, logits, topk_idx, dgate, add, dlogits, stream
     _call(_c.moet_gate_backward, dev, stream, ctypes.byref(p), _ptr("logits", logits, n, _F32, dev),
           _ptr("topk_idx", topk_idx, R, _I32, dev), _ptr("dgate", dgate, R, _F32, dev), _opt("add", add, n, _F32, dev),
           _ptr("dlogits", dlogits, n, _F32, dev))
+
+
+# ---- a dense projection
+
+def moet_linear(p: Problem, x, W, bias, act, residual, u, y, ws, stream=None):
+    dev, T, K, N = _device("x", x), p.T, p.d_model, p.d_expert
+    _call(_c.moet_linear, dev, stream, ctypes.byref(p), _ptr("x", x, T * K, _BF16, dev), _ptr("W", W, K * N, _BF16, dev),
+          _opt("bias", bias, N, _BF16, dev), act, _opt("residual", residual, T * N, _BF16, dev),
+          _opt("u", u, T * N, _BF16, dev), _ptr("y", y, T * N, _BF16, dev), *_ws(ws, dev))
+
+
+def moet_linear_backward(p: Problem, x, W, u, act, dy, dx, dW, dbias, ws, stream=None):
+    dev, T, K, N = _device("dy", dy), p.T, p.d_model, p.d_expert
+    _call(_c.moet_linear_backward, dev, stream, ctypes.byref(p), _opt("x", x, T * K, _BF16, dev),
+          _opt("W", W, K * N, _BF16, dev), _opt("u", u, T * N, _BF16, dev), act, _ptr("dy", dy, T * N, _BF16, dev),
+          _opt("dx", dx, T * K, _BF16, dev), _opt("dW", dW, K * N, _BF16, dev), _opt("dbias", dbias, N, _BF16, dev),
+          *_ws(ws, dev))
 
 
 # ---- the optimizer's step

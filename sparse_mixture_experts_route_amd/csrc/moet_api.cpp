@@ -10,11 +10,28 @@
 #include "../../include/moe_train.h"
 #include "api_common.h"
 #include "internal.h"
+#include "linear.h"
 #include "optim.h"
 
 using namespace moe;
 
 namespace {
+
+float* carve_partials(Carver& c, size_t bytes) { return bytes ? c.take<float>(bytes / sizeof(float)) : nullptr; }
+
+struct LinearBwdWs {
+  uint16_t* du;
+  float *sums, *partials;  // the products follow each other: they share their partial sums
+};
+
+LinearBwdWs carve_linear_backward(Carver& c, const moe_problem_t& p) {
+  LinearBwdWs w;
+  w.du = c.take<uint16_t>((size_t)p.T * p.d_expert);
+  w.sums = c.take<float>((size_t)slope_parts(p.T) * p.d_expert);
+  w.partials = carve_partials(c, std::max(dense_partials_bytes(DENSE_NT, p.T, p.d_model, p.d_expert),
+                                          dense_partials_bytes(DENSE_TN, p.d_model, p.d_expert, p.T)));
+  return w;
+}
 
 size_t stage_bytes(const moe_problem_t& p, int32_t stage) {
   Carver c(nullptr);
@@ -22,7 +39,11 @@ size_t stage_bytes(const moe_problem_t& p, int32_t stage) {
     case MOET_STAGE_DISPATCH:
       carve_permute(c, p);
       break;
+    case MOET_STAGE_LINEAR:
+      carve_partials(c, dense_partials_bytes(DENSE_NN, p.T, p.d_expert, p.d_model));
+      break;
     default:
+      carve_linear_backward(c, p);
       break;
   }
   return c.off + kAlign;  // slack so a 16-byte aligned base can be rounded up to kAlign
@@ -111,6 +132,66 @@ MOE_API moe_status_t moet_gate_backward(const moe_problem_t* p, const float* log
   if (!buffers_ok({in(logits, te), in(topk_idx, R), in(dgate, R), in(add, te), out(dlogits, te)}))
     return MOE_ERR_INVALID_ARGUMENT;
   return hip_status(launch_gate_backward(*p, logits, topk_idx, dgate, add, dlogits, (hipStream_t)stream));
+}
+
+// ---- a dense projection
+
+namespace {
+
+// Operands are reached with 32-bit byte offsets, in whole tiles of up to 256 rows.
+bool linear_supported(const moe_problem_t& p) {
+  const int64_t K = p.d_model, N = p.d_expert, lim = (int64_t)1 << 30;  // of 2 bytes each
+  return p.dtype == MOE_DTYPE_BF16 && p.T * K < lim && p.T * N < lim && K * N < lim && 256 * K < lim && 256 * N < lim;
+}
+
+bool act_ok(int32_t act) { return act >= MOET_ACT_NONE && act <= MOET_ACT_RELU; }
+
+}  // namespace
+
+MOE_API moe_status_t moet_linear(const moe_problem_t* p, const void* x, const void* W, const void* bias, int32_t act,
+                                 const void* residual, void* u, void* y, void* ws, size_t ws_bytes, void* stream) {
+  const moe_status_t st = check_problem(p);
+  if (st != MOE_OK) return st;
+  if (!x || !W || !y || !ws || !act_ok(act)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!linear_supported(*p)) return MOE_ERR_UNSUPPORTED;
+  const size_t T = (size_t)p->T, K = p->d_model, N = p->d_expert, need = stage_bytes(*p, MOET_STAGE_LINEAR);
+  if (!buffers_ok({in(x, T * K * 2), in(W, K * N * 2), in(bias, N * 2), in(residual, T * N * 2), out(u, T * N * 2),
+                   out(y, T * N * 2), out(ws, need)}))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  Carver c(align_ws(ws));
+  float* part = carve_partials(c, dense_partials_bytes(DENSE_NN, p->T, p->d_expert, p->d_model));
+  return hip_status(launch_dense(DENSE_NN, x, W, p->T, p->d_expert, p->d_model, bias, act, residual, u, y, part,
+                                 (hipStream_t)stream));
+}
+
+MOE_API moe_status_t moet_linear_backward(const moe_problem_t* p, const void* x, const void* W, const void* u,
+                                          int32_t act, const void* dy, void* dx, void* dW, void* dbias, void* ws,
+                                          size_t ws_bytes, void* stream) {
+  const moe_status_t st = check_problem(p);
+  if (st != MOE_OK) return st;
+  if (!act_ok(act) || (!u && act != MOET_ACT_NONE) || !dy || !ws || (!dx && !dW && !dbias) || (dx && !W) || (dW && !x))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (!linear_supported(*p)) return MOE_ERR_UNSUPPORTED;
+  const size_t T = (size_t)p->T, K = p->d_model, N = p->d_expert, need = stage_bytes(*p, MOET_STAGE_LINEAR_BACKWARD);
+  if (!buffers_ok({in(x, T * K * 2), in(W, K * N * 2), in(u, T * N * 2), in(dy, T * N * 2), out(dx, T * K * 2),
+                   out(dW, K * N * 2), out(dbias, N * 2), out(ws, need)}))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  hipStream_t s = (hipStream_t)stream;
+  Carver c(align_ws(ws));
+  const LinearBwdWs w = carve_linear_backward(c, *p);
+  const void* du = act == MOET_ACT_NONE ? dy : w.du;
+  hipError_t e = hipSuccess;
+  if (act != MOET_ACT_NONE || dbias)
+    e = launch_slope(dy, u, act, act != MOET_ACT_NONE && (dx || dW) ? w.du : nullptr, dbias, w.sums, p->T, p->d_expert, s);
+  if (e == hipSuccess && dx)
+    e = launch_dense(DENSE_NT, du, W, p->T, p->d_model, p->d_expert, nullptr, MOET_ACT_NONE, nullptr, nullptr, dx,
+                     w.partials, s);
+  if (e == hipSuccess && dW)
+    e = launch_dense(DENSE_TN, x, du, p->d_model, p->d_expert, p->T, nullptr, MOET_ACT_NONE, nullptr, nullptr, dW,
+                     w.partials, s);
+  return hip_status(e);
 }
 
 // ---- the optimizer's step
