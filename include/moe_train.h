@@ -150,14 +150,14 @@ typedef struct {
 } moet_adamw_t;
 
 #define MOET_MAX_TENSORS 1024                 /* of one call */
-#define MOET_GRAD_NORM_WS_BYTES 16640         /* workspace of moet_grad_norm */
+#define MOET_GRAD_NORM_WS_BYTES 8704          /* workspace of moet_grad_norm */
 
 /* One AdamW step, with t = counter[0] + 1 and g = grad grad_scale:
  *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
  *   param -= lr lr_scale lr_factor (m / (1 - beta1^t) / (sqrt(v / (1 - beta2^t)) + eps) + weight_decay param)
  * from the moments before they are rounded, which are taken in 64 bits.
  *   tensors  HOST array of count <= MOET_MAX_TENSORS entries, read during the call only
- *   opt      HOST pointer: finite lr >= 0, beta1 and beta2 in [0, 1), eps >= 1e-30
+ *   opt      HOST pointer: finite lr >= 0, beta1 and beta2 in [0, 1), 1e-15 <= eps <= 1e15
  *   counter  [2] int32: steps taken, and 0, which the call uses. It is advanced by one
  *   lr_scale [1] float32 or NULL: a factor of lr that may change between replays of a captured step
  *   grad_scale [1] float32 or NULL; when it is NaN the step is left out: nothing is written

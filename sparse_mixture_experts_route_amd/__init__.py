@@ -81,3 +81,4 @@ from ._train import (  # noqa: F401
 )
 from .layer import MoEBlockFP8, MoEForward  # noqa: F401
 from .optim import AdamW  # noqa: F401
+from .train_block import MoETrainBlock  # noqa: F401

@@ -25,7 +25,7 @@ MOET_ACT_SILU = 2
 MOET_ACT_RELU = 3
 
 MOET_MAX_TENSORS = 1024
-MOET_GRAD_NORM_WS_BYTES = 16640
+MOET_GRAD_NORM_WS_BYTES = 8704
 
 _c = _lib.raw_lib()
 

@@ -12,7 +12,7 @@ namespace moe {
 enum DenseForm { DENSE_NN, DENSE_NT, DENSE_TN };
 
 struct DensePlan {
-  int tile;    // 0: 256 x 256, 1: 128 x 128, 2: 32 x 128
+  int tile;    // 0: 256 x 256, 1: 128 x 128, 2: 32 x 32, K over the waves
   int splits;  // along K
   int m_tiles, n_tiles, nk, grid;
 };

@@ -112,7 +112,7 @@ template <bool MN, int ROWS>
 __device__ __forceinline__ Slot slot_of(int p) {
   if constexpr (MN) {
     const int k = p / (ROWS / 8);
-    return {((p % (ROWS / 8)) ^ (4 * (k & 3))) * 8, k};
+    return {((p % (ROWS / 8)) ^ (ROWS >= 128 ? 4 * (k & 3) : 0)) * 8, k};
   } else {
     const int row = p / 8;
     return {row, ((p % 8) ^ ((row >> 1) & 7)) * 8};
@@ -127,7 +127,6 @@ __global__ __launch_bounds__(WM * WN * 64, OCC * WM * WN / 4) void dense_kernel(
   constexpr int A_LD = A_STAGE / 1024 / NW, B_LD = B_STAGE / 1024 / NW, NL = A_LD + B_LD;
   constexpr int A_RB = BM * 2, B_RB = BN * 2;  // bytes of a k row (K outermost)
   static_assert(A_LD * 1024 * NW == A_STAGE && B_LD * 1024 * NW == B_STAGE, "whole loads");
-  static_assert((!A_MN || BM >= 128) && (!B_MN || BN >= 128), "the XOR needs 16 chunks");
   constexpr int EP = 32 * 32 * 4;  // a wave's 32 x 32 results
   __shared__ __attribute__((aligned(1024))) char smem[S * STAGE + NW * EP];
 
@@ -390,6 +389,134 @@ __global__ __launch_bounds__(WM * WN * 64, OCC * WM * WN / 4) void dense_kernel(
   }
 }
 
+// Few rows, or few tiles: 32 x 32 results a workgroup, whose 8 waves share the steps
+// along K. Each wave has a ring of its own in LDS and waits for nobody, so up to 128 KB
+// are under way on a CU; the waves' sums meet in LDS in their order, and where the
+// steps need no further cut the results leave in the same launch. (Tiles of 32 x 128 with
+// barriers, always cut, and a second launch: 1 row of 2048 to 8192 12.9 us a call.)
+// A tile of 32 columns with K outermost has rows of 64 bytes: 4 of them are one
+// period of the banks, and a transposing read takes 4 rows as they are.
+constexpr int kThin = 32, kThinWaves = 8, kThinStages = 2;
+
+template <bool A_MN, bool B_MN>
+__global__ __launch_bounds__(kThinWaves * kWave) void thin_kernel(DenseArgs args) {
+  constexpr int OP = kThin * kBK * 2, STAGE = 2 * OP, RING = kThinStages * STAGE, LD = OP / 1024;
+  __shared__ __attribute__((aligned(1024))) char smem[kThinWaves * RING];
+  const int tid = threadIdx.x, lane = tid % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  lds_char* const ring = (lds_char*)smem + wave * RING;
+  const uint32_t ring_addr = lds_addr(smem) + wave * RING;
+
+  // neighbouring tiles along N on one XCD: two of them share a cache line of W
+  const int tiles = args.m_tiles * args.n_tiles, total = tiles * args.splits;
+  const int xcd = blockIdx.x % 8, lo = (int)((int64_t)total * xcd / 8), hi = (int)((int64_t)total * (xcd + 1) / 8);
+  const int item = lo + (int)blockIdx.x / 8;
+  if (item >= hi) return;
+  const int split = item / tiles, t = item - split * tiles, mt = t / args.n_tiles;
+  const int m0 = mt * kThin, n0 = (t - mt * args.n_tiles) * kThin;
+  const int s0 = (int)((int64_t)args.nk * split / args.splits), s1 = (int)((int64_t)args.nk * (split + 1) / args.splits);
+  const int kb = s0 + (s1 - s0) * wave / kThinWaves, kn = s0 + (s1 - s0) * (wave + 1) / kThinWaves - kb;
+
+  i32x4 rsA, rsB;
+  if constexpr (A_MN) rsA = buffer_rsrc(args.A, (uint32_t)((int64_t)args.K * args.lda * 2));
+  else rsA = buffer_rsrc(args.A + (int64_t)m0 * args.lda, (uint32_t)((int64_t)min(args.M - m0, kThin) * args.lda * 2));
+  if constexpr (B_MN) rsB = buffer_rsrc(args.B, (uint32_t)((int64_t)args.K * args.ldb * 2));
+  else rsB = buffer_rsrc(args.B + (int64_t)n0 * args.ldb, (uint32_t)((int64_t)kThin * args.ldb * 2));
+  uint32_t a_off[LD], b_off[LD];
+#pragma unroll
+  for (int l = 0; l < LD; ++l) {
+    const Slot a = slot_of<A_MN, kThin>(l * kWave + lane), b = slot_of<B_MN, kThin>(l * kWave + lane);
+    a_off[l] = A_MN ? (uint32_t)(a.k * args.lda + m0 + a.row) * 2u : (uint32_t)(a.row * args.lda + a.k) * 2u;
+    b_off[l] = B_MN ? (uint32_t)(b.k * args.ldb + n0 + b.row) * 2u : (uint32_t)(b.row * args.ldb + b.k) * 2u;
+  }
+  auto issue = [&](int step) {
+    const uint32_t st = ring_addr + (step % kThinStages) * STAGE, k = (uint32_t)(kb + step) * kBK;
+#pragma unroll
+    for (int l = 0; l < LD; ++l) buffer_load_lds16(rsB, b_off[l], k * (B_MN ? (uint32_t)args.ldb * 2u : 2u), st + OP + l * 1024);
+#pragma unroll
+    for (int l = 0; l < LD; ++l) buffer_load_lds16(rsA, a_off[l], k * (A_MN ? (uint32_t)args.lda * 2u : 2u), st + l * 1024);
+  };
+  const int q = lane & 15, g = lane >> 4;
+  const int mn_rd = ((g >> 1) * 8 + (q >> 2)) * (kThin * 2) + ((g & 1) * 16 + (q & 3) * 4) * 2;
+  auto fragment = [&](const lds_char* op, bool mn, int ks) {
+    if (mn) {
+      const lds_char* const p = op + ks * 16 * (kThin * 2) + mn_rd;
+      const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+      const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * (kThin * 2)));
+      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+    const int row = lane & 31;
+    return *(const lds_bf16x8*)(op + row * (kBK * 2) + (((ks * 2 + (lane >> 5)) ^ ((row >> 1) & 7)) << 4));
+  };
+
+  f32x16 acc;
+#pragma unroll
+  for (int v = 0; v < 16; ++v) acc[v] = 0.0f;
+#pragma unroll
+  for (int s = 0; s < kThinStages; ++s)
+    if (s < kn) issue(s);
+  for (int kt = 0; kt < kn; ++kt) {
+    if (kt + 1 < kn) wait_vmem<2 * LD>();  // the next step's loads alone may be under way
+    else wait_vmem<0>();
+    const lds_char* const st = ring + (kt % kThinStages) * STAGE;
+    bf16x8 a[kKS], b[kKS];
+#pragma unroll
+    for (int ks = 0; ks < kKS; ++ks) {
+      a[ks] = fragment(st, A_MN, ks);
+      b[ks] = fragment(st + OP, B_MN, ks);
+    }
+    if (kt + kThinStages < kn) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wave's reads are through
+      issue(kt + kThinStages);
+    }
+#pragma unroll
+    for (int ks = 0; ks < kKS; ++ks) acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[ks], a[ks], acc, 0, 0, 0);
+  }
+  // a lane's sums: row lane & 31, columns 8 v + 4 (lane >> 5) .. + 3
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const int row = lane & 31, ch = v * 2 + (lane >> 5);
+    *(__attribute__((address_space(3))) f32x4*)(ring + row * 128 + ((ch ^ (row & 7)) << 4)) =
+        f32x4{acc[4 * v], acc[4 * v + 1], acc[4 * v + 2], acc[4 * v + 3]};
+  }
+  __syncthreads();
+  const int row = tid / 8, ch = tid % 8;  // 4 columns a thread
+  if (row >= kThin || m0 + row >= args.M) return;
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int w = 0; w < kThinWaves; ++w)
+    sum += *(__attribute__((address_space(3))) f32x4*)((lds_char*)smem + w * RING + row * 128 + ((ch ^ (row & 7)) << 4));
+  const int col = n0 + ch * 4;
+  const int64_t off = (int64_t)(m0 + row) * args.N + col;
+  if (args.splits > 1) {
+    *(f32x4*)(args.partials + (int64_t)split * args.M * args.N + off) = sum;
+    return;
+  }
+  const Epilogue& E = args.ep;
+  auto widen4 = [](const bf16_bits* p, float* f) {
+    const u32x2 v = *(const u32x2*)p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = bf16_to_f32(i & 1 ? v[i / 2] >> 16 : v[i / 2] & 0xFFFFu);
+  };
+  float f[4], w[4];
+#pragma unroll
+  for (int v = 0; v < 4; ++v) f[v] = sum[v];
+  if (E.bias) {
+    widen4(E.bias + col, w);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) f[v] += w[v];
+  }
+  if (E.u) *(u32x2*)(E.u + off) = u32x2{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])};
+#pragma unroll
+  for (int v = 0; v < 4; ++v) f[v] = act_of(f[v], E.act);
+  if (E.residual) {
+    widen4(E.residual + off, w);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) f[v] += w[v];
+  }
+  *(u32x2*)(E.y + off) = u32x2{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])};
+}
+
 // The cut tiles' sums in split order, 8 columns a thread
 __global__ __launch_bounds__(256) void dense_join_kernel(const float* __restrict__ partials, Epilogue E, int64_t M, int N,
                                                          int splits) {
@@ -486,32 +613,40 @@ __global__ __launch_bounds__(256) void dbias_kernel(const float* __restrict__ su
 
 }  // namespace
 
+// The tile and the cut along K by estimated time, us, fitted to 16 shapes in three forms
+// (rows 1 to 8192, widths 64 to 8192; within 15% of what they take, and of the best
+// choice). Measured for x W, best of each tile: 32 rows of 2048 to 8192 21 / 16.4 / 12.4,
+// 512 of 2048 to 2048 29.7 / 23.8 / 31.9, 2048 of 2048 to 2048 51 / 39.8 / over 100, 8192 of 2048
+// to 8192 265 / 303 / -.
 DensePlan dense_plan(DenseForm form, int64_t M, int64_t N, int64_t K) {
+  static const int edge[3] = {256, 128, kThin};
   const int cus = device_cus() / 8 * 8;
   const int64_t nk = ceil_div(K, (int64_t)kBK);
-  const char* force = getenv("MOE_LINEAR_TILE");
+  // MOE_LINEAR_TILE=0|1|2 and MOE_LINEAR_SPLITS=<power of two> force the choice where it is possible
+  const char *ft = getenv("MOE_LINEAR_TILE"), *fs = getenv("MOE_LINEAR_SPLITS");
+  const int64_t most = max((int64_t)1, nk / 4);  // at least four steps of a cut tile
   DensePlan best{};
   double best_us = 1e30;
   for (int tile = 0; tile < 3; ++tile) {
-    static const int bm[3] = {256, 128, 32}, bn[3] = {256, 128, 128}, per_cu[3] = {1, 2, 2};
-    static const double step_us[3] = {1.95, 1.6, 1.0};
-    if (tile == 2 && form == DENSE_TN) continue;
-    if (force && force[0] && atoi(force) != tile && !(tile == 1 && atoi(force) == 2 && form == DENSE_TN)) continue;
-    const int64_t mt = ceil_div(M, (int64_t)bm[tile]), nt = ceil_div(N, (int64_t)bn[tile]), tiles = mt * nt;
-    const int64_t slots = (int64_t)cus * per_cu[tile];
-    for (int64_t splits = 1; splits <= 32 && splits <= max((int64_t)1, nk / 4); splits *= 2) {
-      const int64_t items = tiles * splits, rounds = ceil_div(items, slots);
-      const double us = rounds * ceil_div(nk, splits) * step_us[tile] +
-                        (splits > 1 ? 3.0 + 8.0 * M * N * splits / 4e6 : 0.0);
-      if (items >= INT32_MAX / 2) continue;
+    if (ft && ft[0] && atoi(ft) != tile) continue;
+    const int64_t mt = ceil_div(M, (int64_t)edge[tile]), nt = ceil_div(N, (int64_t)edge[tile]);
+    for (int64_t splits = 1; splits <= 32 && splits <= most; splits *= 2) {
+      const int64_t items = mt * nt * splits, steps = ceil_div(nk, splits);
+      if (items >= (int64_t)1 << 22) continue;  // less than 2^32 threads, 8 for each a multiple
+      if (fs && fs[0] && splits > 1 && splits > atoi(fs)) continue;
+      double us, base;
+      if (tile == 0) base = 5.0, us = ceil_div(items, (int64_t)cus) * steps * 2.05;
+      else if (tile == 1)
+        base = 4.0, us = steps * (items <= cus ? 0.75 + 0.33 * items / cus : ceil_div(items, (int64_t)2 * cus) * 1.25);
+      else
+        base = 3.0, us = max(1.0, (double)items / cus) * steps * (form == DENSE_NN ? 0.22 : form == DENSE_NT ? 0.18 : 0.25);
+      us = base + max(us, 2.0 * (M * K + K * N) / 4.2e6);  // the operands have to come in
+      if (splits > 1) us += 3.0 + 8.0 * M * N * splits / 5.5e6;  // partial sums out and in, and their launch
+      if (fs && fs[0]) us = -(double)splits;
       if (us < best_us) {
         best_us = us;
-        best.tile = tile;
-        best.splits = (int)splits;
-        best.m_tiles = (int)mt;
-        best.n_tiles = (int)nt;
-        best.nk = (int)nk;
-        best.grid = (int)(min(items, slots) + 7) / 8 * 8;
+        best = {tile, (int)splits, (int)mt, (int)nt, (int)nk,
+                (int)((tile == 0 ? min(items, (int64_t)cus) : tile == 1 ? min(items, (int64_t)2 * cus) : items) + 7) / 8 * 8};
       }
     }
   }
@@ -549,15 +684,18 @@ hipError_t launch_dense(DenseForm form, const void* A, const void* B, int64_t M,
     if (form == DENSE_NN) MOE_DENSE(false, true, BM, BN, WM, WN, S, OCC);  \
     else MOE_DENSE(false, false, BM, BN, WM, WN, S, OCC);             \
   } while (0)
-  if (form == DENSE_TN) {
+  if (p.tile == 2) {
+    hipLaunchKernelGGL((form == DENSE_NN   ? thin_kernel<false, true>
+                        : form == DENSE_NT ? thin_kernel<false, false>
+                                           : thin_kernel<true, true>),
+                       dim3((unsigned)p.grid), dim3(kThinWaves * kWave), 0, s, a);
+  } else if (form == DENSE_TN) {
     if (p.tile == 0) MOE_DENSE(true, true, 256, 256, 2, 4, 2, 1);
     else MOE_DENSE(true, true, 128, 128, 2, 2, 2, 2);
   } else if (p.tile == 0) {
     MOE_DENSE_FORM(256, 256, 2, 4, 2, 1);
-  } else if (p.tile == 1) {
-    MOE_DENSE_FORM(128, 128, 2, 2, 2, 2);
   } else {
-    MOE_DENSE_FORM(32, 128, 1, 4, 3, 2);
+    MOE_DENSE_FORM(128, 128, 2, 2, 2, 2);
   }
 #undef MOE_DENSE_FORM
 #undef MOE_DENSE

@@ -248,7 +248,7 @@ MOE_API moe_status_t moet_adamw(const moet_tensor_t* tensors, int32_t count, con
   if (!opt || !counter) return MOE_ERR_INVALID_ARGUMENT;
   const double b1 = opt->beta1, b2 = opt->beta2;
   if (!std::isfinite(opt->lr) || opt->lr < 0 || !(b1 >= 0 && b1 < 1) || !(b2 >= 0 && b2 < 1) ||
-      !std::isfinite(opt->eps) || opt->eps < 1e-30 || opt->eps > 1e30)
+      !std::isfinite(opt->eps) || opt->eps < 1e-15 || opt->eps > 1e15)
     return MOE_ERR_INVALID_ARGUMENT;
   const int64_t total = list_values(tensors, count);
   if (total == -1) return MOE_ERR_INVALID_ARGUMENT;

@@ -118,45 +118,57 @@ __device__ __forceinline__ void decode8(const u32x2& q, float* f) {
 // 2^e in 64 bits
 __device__ __forceinline__ double pow2(int e) { return __longlong_as_double((long long)(1023 + e) << 52); }
 
-// The smallest float32 that is not below |x|
+// The smallest float32 that is not below x >= 0
 __device__ __forceinline__ float up32(double x) {
-  const float f = (float)fabs(x);
-  return (double)f < fabs(x) && f < INFINITY ? __uint_as_float(__float_as_uint(f) + 1u) : f;
+  const float f = (float)x;
+  return (double)f < x && f < INFINITY ? __uint_as_float(__float_as_uint(f) + 1u) : f;
 }
 
-// A scaled value to its code with random number r < 2^16: e4m3 (3 bits of
-// mantissa, bias 7) or e5m2 (2 bits, bias 15). The spacing at a normal value is
-// its exponent's, so floor(|x| / s + r / 2^16) is an addition to the bits below
-// the mantissa kept: those in the upper half of the double are enough, as r ends
-// above the others. Subnormal codes count units of the smallest spacing.
+// Code of x / 2^e with random number r < 2^16: e4m3 (3 bits of mantissa, bias 7) or
+// e5m2 (2 bits, bias 15). x is sig 2^(exp - 20) with 21 bits of sig from the double's
+// upper half; shifted to units of 2^-16 spacings, below the smallest normal those of
+// that one, floor(|x| / s + r / 2^16) is an integer sum. The lower half of the
+// double lies below those units and cannot change the floor.
 template <bool E5>
-__device__ __forceinline__ uint32_t encode(double x, uint32_t r) {
-  constexpr int M = E5 ? 2 : 3, BIAS = E5 ? 15 : 7, CUT = 20 - M;
-  const double a = fabs(x);
-  const uint32_t hi = (uint32_t)__double2hiint(x) & 0x7FFFFFFFu;
-  uint32_t c = ((hi + (r << (CUT - 16))) >> CUT) - ((uint32_t)(1023 - BIAS) << M);
-  if (a < pow2(1 - BIAS)) c = ((uint32_t)(a * pow2(BIAS - 1 + M + 16)) + r) >> 16;
-  if (E5 && c == 0u && a > 0.0) c = 1u;  // a second moment that is not 0
-  if (!(a <= (E5 ? 57344.0 : 448.0))) c = 0x7Fu;
-  return E5 ? c : c | (((uint32_t)__double2hiint(x) >> 24) & 0x80u);
+__device__ __forceinline__ uint32_t encode(double x, int e, uint32_t r) {
+  constexpr int M = E5 ? 2 : 3, BIAS = E5 ? 15 : 7;
+  constexpr uint32_t TOP = E5 ? 0x40EC0000u : 0x407C0000u;  // upper halves of 57344.0 and 448.0
+  const uint32_t full = (uint32_t)__double2hiint(x), hi = full & 0x7FFFFFFFu;
+  const int up = (int)(hi >> 20) - (1024 - BIAS + e);  // exponent above that of the smallest normal
+  const uint32_t sig = (hi & 0xFFFFFu) | 0x100000u;
+  uint32_t c = ((sig >> min(4 - M + max(-up, 0), 31)) + r) >> 16;
+  c += (uint32_t)max(up, 0) << M;
+  if (E5) c = x > 0.0 ? max(c, 1u) : c;  // a second moment that is not 0
+  if (hi > TOP + (uint32_t)(e << 20)) c = 0x7Fu;
+  return E5 ? c : c | ((full >> 24) & 0x80u);
+}
+
+// b m + c d, products and sum rounded one by one: the same bits wherever they are computed.
+// (A fused one is a step off in 64 bits; where the sum lies on a border of two codes, as
+// one in five does for short factors, that would show.)
+__device__ __forceinline__ double moment(double b, double m, double c, double d) {
+#pragma clang fp contract(off)
+  return b * m + c * d;
 }
 
 struct Hyper {
   double b1, b2, gs;
-  float step, root, lr, eps;  // lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
+  float step, root, decay, eps;  // lr / (1 - b1^t), 1 / sqrt(1 - b2^t), lr weight_decay
   uint32_t key;
 };
 
-template <bool G16, bool P16, bool S8>
-__device__ __forceinline__ void update(const OptTensor& T, const Hyper& h, int64_t i0) {
+// WHOLE: the workgroup's chunk ends inside the tensor. All loads then go out together; with
+// the tail's branches between them the first was waited for before the second left.
+template <bool G16, bool P16, bool S8, bool WHOLE>
+__device__ __forceinline__ void update_chunk(const OptTensor& T, const Hyper& h, int64_t i0) {
   const int64_t n = T.n;
-  const bool whole = i0 + kVals <= n;
+  const bool whole = WHOLE || i0 + kVals <= n;
   float g[kVals], p[kVals], mf[kVals], vf[kVals];
   double m[kVals], v[kVals];
   load_vals<G16>(T.grad, i0, n, whole, g);
   load_vals<false>(P16 ? T.master : (const float*)T.param, i0, n, whole, p);
   const int64_t block = i0 / kQBlock;
-  const bool inside = i0 < n;
+  const bool inside = WHOLE || i0 < n;
   if constexpr (S8) {
     const u32x2 mq = load_codes(T.m, i0, n, whole), vq = load_codes(T.v, i0, n, whole);
     const double ms = pow2(inside ? (int)T.m_scale[block] - 127 : 0), vs = pow2(inside ? (int)T.v_scale[block] - 127 : 0);
@@ -179,43 +191,41 @@ __device__ __forceinline__ void update(const OptTensor& T, const Hyper& h, int64
 #pragma unroll
   for (int i = 0; i < kVals; ++i) {
     const double d = (double)g[i] * h.gs;
-    // products and sums rounded one by one: the same bits wherever they are computed
-    m[i] = __dadd_rn(__dmul_rn(h.b1, m[i]), __dmul_rn(1.0 - h.b1, d));
-    v[i] = __dadd_rn(__dmul_rn(h.b2, v[i]), __dmul_rn(__dmul_rn(1.0 - h.b2, d), d));
+    m[i] = moment(h.b1, m[i], 1.0 - h.b1, d);
+    v[i] = moment(h.b2, v[i], (1.0 - h.b2) * d, d);
     mf[i] = (float)m[i];
     vf[i] = (float)v[i];
-    const float move = h.step * mf[i] / (sqrtf(vf[i]) * h.root + h.eps);
-    p[i] = p[i] - fmaf(h.lr * T.weight_decay, p[i], move);
+    // the hardware's root and reciprocal, each within a unit in the last place: the move is
+    // a small part of p (with eps >= 1e-15 a root that it takes for 0 does not count)
+    const float move = h.step * mf[i] * __builtin_amdgcn_rcpf(fmaf(__builtin_amdgcn_sqrtf(vf[i]), h.root, h.eps));
+    p[i] = p[i] - fmaf(h.decay, p[i], move);
   }
   store_vals<false>(P16 ? (void*)T.master : T.param, i0, n, whole, p);
   if constexpr (P16) store_vals<true>(T.param, i0, n, whole, p);
   if constexpr (S8) {
-    float mt = 0.0f, vt = 0.0f;
+    double mt = 0.0, vt = 0.0;
 #pragma unroll
-    for (int i = 0; i < kVals; ++i) {
-      if (i0 + i < n) {
-        mt = fmaxf(mt, up32(m[i]));
-        vt = fmaxf(vt, up32(v[i]));
-      }
+    for (int i = 0; i < kVals; ++i) {  // values past the end are 0
+      mt = fmax(mt, fabs(m[i]));
+      vt = fmax(vt, v[i]);
     }
     // the lanes of a DPP row have the 128 values of a scale; 57344 is 1.75 2^15, 448 is 1.75 2^8
-    const int mb = scale_byte(row16_max(mt));
-    const uint32_t vu = __float_as_uint(row16_max(vt));
-    const int vb = min(max((int)((vu + 0x1FFFFFu) >> 23) - 142, -120), 120) + 127;
-    const double mi = pow2(127 - mb), vi = pow2(127 - vb);
+    const int me = scale_byte(row16_max(up32(mt))) - 127;
+    const uint32_t vu = __float_as_uint(row16_max(up32(vt)));
+    const int ve = min(max((int)((vu + 0x1FFFFFu) >> 23) - 142, -120), 120);
     u32x2 mq = {0u, 0u}, vq = {0u, 0u};
     const uint32_t high = (uint32_t)((uint64_t)i0 >> 32) * 0x9E3779B9u;  // a chunk does not cross 2^32
 #pragma unroll
     for (int i = 0; i < kVals; ++i) {
       const uint32_t r = mix32(((uint32_t)(i0 + i) + h.key) ^ high);
-      mq[i / 4] |= encode<false>(m[i] * mi, r & 0xFFFFu) << (8 * (i % 4));
-      vq[i / 4] |= encode<true>(v[i] * vi, r >> 16) << (8 * (i % 4));
+      mq[i / 4] |= encode<false>(m[i], me, r & 0xFFFFu) << (8 * (i % 4));
+      vq[i / 4] |= encode<true>(v[i], ve, r >> 16) << (8 * (i % 4));
     }
     store_codes(T.m, i0, n, whole, mq);
     store_codes(T.v, i0, n, whole, vq);
     if (inside && i0 % kQBlock == 0) {
-      T.m_scale[block] = (uint8_t)mb;
-      T.v_scale[block] = (uint8_t)vb;
+      T.m_scale[block] = (uint8_t)(me + 127);
+      T.v_scale[block] = (uint8_t)(ve + 127);
     }
   } else {
     store_vals<false>(T.m, i0, n, whole, mf);
@@ -223,10 +233,18 @@ __device__ __forceinline__ void update(const OptTensor& T, const Hyper& h, int64
   }
 }
 
-// Index of the tensor that chunk c is of: the last whose first chunk is not above it
+template <bool G16, bool P16, bool S8>
+__device__ __forceinline__ void update(const OptTensor& T, const Hyper& h, int64_t first) {
+  const int64_t i0 = first + threadIdx.x * kVals;
+  if (first + kOptChunk <= T.n) update_chunk<G16, P16, S8, true>(T, h, i0);
+  else update_chunk<G16, P16, S8, false>(T, h, i0);
+}
+
+// Index of the tensor that chunk c is of, not before `from`: the last whose first chunk is not above it
 template <typename L>
-__device__ __forceinline__ int tensor_of(const L& l, int c) {
-  int a = 0, b = l.count;
+__device__ __forceinline__ int tensor_of(const L& l, int c, int from = 0) {
+  if (from + 1 >= l.count || l.t[from + 1].first > c) return from;
+  int a = from + 1, b = l.count;
   while (b - a > 1) {
     const int mid = (a + b) >> 1;
     if (l.t[mid].first <= c) a = mid;
@@ -247,20 +265,22 @@ __global__ __launch_bounds__(kOptThreads) void adamw_kernel(const OptList l, con
     const double c1 = -expm1(t * o.log_beta1), c2 = -expm1(t * o.log_beta2);
     const double lr = o.lr * (lr_scale ? (double)*lr_scale : 1.0);
     const uint32_t draw = (uint32_t)(before + 1) * 0x9E3779B9u;
-    for (int c = blockIdx.x; c < l.chunks; c += gridDim.x) {
-      const int j = tensor_of(l, c);
+    Hyper h;
+    h.b1 = o.beta1;
+    h.b2 = o.beta2;
+    h.gs = gs;
+    h.root = (float)(1.0 / sqrt(c2));
+    h.eps = o.eps;
+    // Workgroups side by side take neighbouring chunks: ranges of their own, all at the
+    // same place of the memory channels' period at a time, took 28% longer for the norm.
+    for (int c = blockIdx.x, j = 0; c < l.chunks; c += gridDim.x) {
+      j = tensor_of(l, c, j);
       const OptTensor& T = l.t[j];
       const double f = lr * (double)T.lr_factor;
-      Hyper h;
-      h.b1 = o.beta1;
-      h.b2 = o.beta2;
-      h.gs = gs;
       h.step = (float)(f / c1);
-      h.root = (float)(1.0 / sqrt(c2));
-      h.lr = (float)f;
-      h.eps = o.eps;
+      h.decay = (float)(f * (double)T.weight_decay);
       h.key = mix32(o.seed + mix32(draw + (uint32_t)(l.base + j)));
-      const int64_t i0 = (int64_t)(c - T.first) * kOptChunk + threadIdx.x * kVals;
+      const int64_t i0 = (int64_t)(c - T.first) * kOptChunk;
       switch (T.flags) {  // the same for the whole workgroup
         case 0: update<false, false, false>(T, h, i0); break;
         case kGrad16: update<true, false, false>(T, h, i0); break;
@@ -275,10 +295,11 @@ __global__ __launch_bounds__(kOptThreads) void adamw_kernel(const OptList l, con
   }
   if (!l.last) return;
   // The last workgroup to come here advances the counter: all have read it by then,
-  // this one's other waves included.
+  // this one's other waves included (the barrier waits for their loads). Nothing else
+  // is passed on, so no fence: one of the device's scope writes the L2 back.
   __syncthreads();
   if (threadIdx.x == 0) {
-    const int32_t n = __hip_atomic_fetch_add(counter + 1, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    const int32_t n = __hip_atomic_fetch_add(counter + 1, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if (n == (int32_t)gridDim.x - 1) {
       __hip_atomic_store(counter + 1, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       if (!skip) __hip_atomic_store(counter, before + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -298,14 +319,46 @@ __device__ __forceinline__ double block_sum(double v, double* slots) {
 __global__ __launch_bounds__(kOptThreads) void square_sums_kernel(const NormList l, double* __restrict__ slots) {
   __shared__ double s_v[kOptThreads / kWave];
   double sum = 0.0;
-  for (int c = blockIdx.x; c < l.chunks; c += gridDim.x) {
-    const NormTensor& T = l.t[tensor_of(l, c)];
-    const int64_t i0 = (int64_t)(c - T.first) * kOptChunk + threadIdx.x * kVals;
-    float g[kVals];
-    if (T.flags) load_vals<true>(T.grad, i0, T.n, i0 + kVals <= T.n, g);
-    else load_vals<false>(T.grad, i0, T.n, i0 + kVals <= T.n, g);
+  constexpr int U = 4;  // chunks under way together
+  int j = 0;
+  for (int c0 = blockIdx.x; c0 < l.chunks; c0 += gridDim.x * U) {
+    u32x4 q[U][2];
+    uint32_t b16[U];
 #pragma unroll
-    for (int i = 0; i < kVals; ++i) sum = fma((double)g[i], (double)g[i], sum);
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + u * (int)gridDim.x;
+      b16[u] = 0;
+      q[u][0] = q[u][1] = u32x4{0u, 0u, 0u, 0u};
+      if (c >= l.chunks) continue;
+      j = tensor_of(l, c, j);
+      const NormTensor& T = l.t[j];
+      const int64_t first = (int64_t)(c - T.first) * kOptChunk, i = first + threadIdx.x * kVals;
+      b16[u] = T.flags;
+      if (first + kOptChunk <= T.n) {
+        if (T.flags) {
+          q[u][0] = *(const u32x4*)((const bf16_bits*)T.grad + i);
+        } else {
+          const u32x4* p = (const u32x4*)((const float*)T.grad + i);
+          q[u][0] = p[0];
+          q[u][1] = p[1];
+        }
+      } else {
+        b16[u] = 0;
+        float g[kVals];
+        if (T.flags) load_vals<true>(T.grad, i, T.n, i + kVals <= T.n, g);
+        else load_vals<false>(T.grad, i, T.n, i + kVals <= T.n, g);
+#pragma unroll
+        for (int v = 0; v < kVals; ++v) q[u][v / 4][v % 4] = __float_as_uint(g[v]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int i = 0; i < kVals; ++i) {
+        const double g = __uint_as_float(!b16[u] ? q[u][i / 4][i % 4] : (i & 1) ? q[u][0][i / 2] & 0xFFFF0000u : q[u][0][i / 2] << 16);
+        sum = fma(g, g, sum);
+      }
+    }
   }
   sum = block_sum(sum, s_v);
   if (threadIdx.x == 0) slots[blockIdx.x] = l.add ? slots[blockIdx.x] + sum : sum;

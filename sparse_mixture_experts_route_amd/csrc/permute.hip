@@ -178,12 +178,56 @@ __global__ __launch_bounds__(kScanThreads) void scan_kernel(const int32_t* __res
 // separate scan launch is skipped.
 constexpr int kFusedScanBlocks = 64;
 
+// Rows of a block in which a token names an expert more than once. Level m has the bits
+// of the tokens that name an expert m times or more: a selection's rank is the sum over the
+// levels of the bits below its token, and the token's own earlier ones.
+// (Ranks are added up in inv; a token's entries are its own thread's.)
+__device__ __noinline__ void scatter_repeats(const int32_t* __restrict__ idx, int64_t T, int k, int E, int64_t t,
+                                             uint32_t (*mask)[kWords], const int32_t* s_base,
+                                             int32_t* __restrict__ perm, int32_t* inv) {
+  const int w = threadIdx.x >> 5;
+  const uint32_t bit = 1u << (threadIdx.x & 31);
+  auto named = [&](int j) { return t < T ? idx[t * k + j] : -1; };
+  auto before = [&](int j, int e) {  // the token's selections of e ahead of j
+    int n = 0;
+    for (int i = 0; i < j; ++i) n += idx[t * k + i] == e;
+    return n;
+  };
+  for (int m = 0;; ++m) {
+    __syncthreads();
+    uint32_t* flat = &mask[0][0];
+    for (int i = threadIdx.x; i < E * kWords; i += kTB) flat[i] = 0u;
+    __syncthreads();
+    bool more = false;
+    for (int j = 0; j < k; ++j) {
+      const int e = named(j);
+      if ((unsigned)e >= (unsigned)E) continue;
+      const int n = before(j, e);
+      if (n == m) atomicOr(&mask[e][w], bit);
+      more |= n > m;
+    }
+    more = __syncthreads_or(more);
+    for (int j = 0; j < k; ++j) {
+      const int e = named(j);
+      if (t >= T) break;
+      int r = -1;
+      if ((unsigned)e < (unsigned)E) {
+        r = m == 0 ? s_base[e] + before(j, e) : inv[t * k + j];
+        r += __popc(mask[e][w] & (bit - 1u));
+        for (int i = 0; i < w; ++i) r += __popc(mask[e][i]);
+        if (!more) perm[r] = (int32_t)t;
+      }
+      inv[t * k + j] = r;
+    }
+    if (!more) return;
+  }
+}
+
 // SCAN: `blockcounts` holds the per-block counts of hist_kernel (nb blocks);
 // every block sums them per expert (in total and over the blocks before it),
 // scans the totals over the experts, and block 0 writes counts and offsets.
 // Otherwise `blockcounts` is scan_kernel's first row of every (block, expert).
-// REPEATS: where a token of the block names an expert twice, ranks are counted
-// over the block's selections instead of read from the masks.
+// REPEATS: a token may name an expert more than once (scatter_repeats).
 template <bool SCAN, bool REPEATS>
 __global__ __launch_bounds__(kTB) void scatter_kernel(const int32_t* __restrict__ idx, int64_t T, int k, int E,
                                                       const int32_t* __restrict__ blockcounts, int64_t nb,
@@ -230,20 +274,11 @@ __global__ __launch_bounds__(kTB) void scatter_kernel(const int32_t* __restrict_
   // this block's first row per expert is visible after build_mask's barriers
   const bool repeated = build_mask<REPEATS>(idx, T, k, E, mask, t0, extra);
   const int64_t t = t0 + threadIdx.x;
-  if (t >= T) return;
   if (REPEATS && repeated) {
-    for (int j = 0; j < k; ++j) {
-      const int e = idx[t * k + j];
-      int32_t r = -1;
-      if ((unsigned)e < (unsigned)E) {
-        r = s_base[e];
-        for (int64_t i = t0 * k; i < t * k + j; ++i) r += idx[i] == e;
-        perm[r] = (int32_t)t;
-      }
-      inv[t * k + j] = r;
-    }
+    scatter_repeats(idx, T, k, E, t, mask, s_base, perm, inv);
     return;
   }
+  if (t >= T) return;
   const int w = threadIdx.x >> 5;
   const uint32_t below = (1u << (threadIdx.x & 31)) - 1u;
   // the selections in groups of 8, whose indices are loaded together

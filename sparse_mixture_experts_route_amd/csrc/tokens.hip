@@ -282,7 +282,9 @@ __global__ __launch_bounds__(kThreads) void from_rows_kernel(const u32x4* __rest
 // Index and rows of a few selections in one launch: workgroup (t, part) counts the
 // selections before its token's own ones in the order of the rows, P compares for
 // each, and writes its part of their rows; one more workgroup counts the experts.
-constexpr int kSmallSelections = 2048;
+// Against histograms, ranks and rows in three launches, us in a graph: 32 tokens of 8
+// selections 5.6 / 11.9, 512 of 8 14.4 / 18.6, 1024 of 2 9.9 / 11.7, 1024 of 4 14.6 / 14.6,
+// 2048 of 2 22.5 / 11.9.
 constexpr int kSmallPart = 2 * kThreads;  // 16-byte pieces of a row per workgroup
 
 template <bool BF16>
@@ -459,14 +461,15 @@ bool streams(const moe_problem_t& p) {
   return (double)p.T * p.k * p.d_model * (p.dtype == MOE_DTYPE_BF16 ? 2 : 4) >= (double)(128 << 20);
 }
 
-// Waves of a token whose dot products are wanted
-int dot_waves(const moe_problem_t& p, int64_t row_vecs) { return p.T >= 2048 || row_vecs <= kWave ? 1 : kWaves; }
+// Waves of a token whose dot products are wanted: one where the tokens fill the chip or
+// a row is one step of a wave
+int dot_waves(const moe_problem_t& p, int64_t row_vecs) { return p.T >= 2048 || row_vecs <= kStep ? 1 : kWaves; }
 
 unsigned grid_of(int64_t waves) { return (unsigned)min(ceil_div(waves, (int64_t)kWaves), kMostBlocks); }
 
 }  // namespace
 
-bool dispatch_small(const moe_problem_t& p) { return p.T * p.k <= kSmallSelections; }
+bool dispatch_small(const moe_problem_t& p) { return p.T <= 1024 && p.T * p.T * p.k <= (int64_t)1 << 21; }
 
 hipError_t launch_dispatch_small(const moe_problem_t& p, const int32_t* idx, const float* w, const void* x,
                                  int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv, void* x_perm,

@@ -7,6 +7,7 @@ from typing import Optional, Sequence
 import torch
 
 from . import _ext, _train
+from .layer import _torch_stream
 
 _KINDS = ("master", "m", "m_scale", "v", "v_scale")
 
@@ -27,7 +28,10 @@ class AdamW:
 
     state: buffers to go on from, lists by the names master, m, m_scale, v, v_scale
     (None where a parameter has none) and counter, as `state` gives them; they are
-    used in place. All calls of an object are on one stream, or ordered by the caller.
+    used in place. All calls of an object are on one stream, or ordered by the caller;
+    it is ready for any stream when it has been made. Its own buffers' memory is not
+    handed out again while work of a torch stream is in flight on it; for a raw stream
+    handle the caller keeps the object until that work has ended.
     """
 
     def __init__(self, params: Sequence[torch.Tensor], lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
@@ -48,10 +52,10 @@ class AdamW:
                 raise ValueError(f"{len(v)} values of {name} for {n} parameters")
             return v
 
-        given = isinstance(bits, (list, tuple))
-        width = [b if given or p.numel() >= least else 32 for b, p in zip(each(bits, "bits"), self.params)]
+        given, width = isinstance(bits, (list, tuple)), each(bits, "bits")
         if any(b not in (8, 32) for b in width):
             raise ValueError("moments are held in 8 or in 32 bits")
+        width = [b if given or p.numel() >= least else 32 for b, p in zip(width, self.params)]
         if state is None:
             state = self._fresh(width)
         missing = [k for k in (*_KINDS, "counter") if k not in state]
@@ -70,6 +74,21 @@ class AdamW:
             self.lr_scale = torch.ones(1, device=self.device)
             self.norm, self.scale = (torch.ones(1, device=self.device) for _ in range(2))
             self._ws = torch.empty(_train.MOET_GRAD_NORM_WS_BYTES, dtype=torch.uint8, device=self.device)
+        self._known = {_ext._handle(self.device.index, None)}  # streams that the allocator knows to use the buffers
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(self.device).synchronize()
+
+    def _keep(self, stream):
+        """Tells the allocator, once for each, of the torch streams that use the buffers besides their own."""
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            return
+        handle = _ext._handle(self.device.index, stream)
+        if handle not in self._known:
+            self._known.add(handle)
+            s = _torch_stream(self.device, stream)
+            for t in (self.counter, self.lr_scale, self.norm, self.scale, self._ws, *(t for k in _KINDS for t in getattr(self, k))):
+                if t is not None:
+                    t.record_stream(s)
 
     def _fresh(self, width):
         s = {k: [] for k in _KINDS}
@@ -95,6 +114,7 @@ class AdamW:
         gradients before clipping (this object's buffer), None without max_norm."""
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
+        self._keep(stream)
         dev = self.device.index
         for e, g in zip(self._list, grads):
             _train.set_grad(e, g, dev)
