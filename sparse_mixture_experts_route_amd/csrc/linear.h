@@ -21,8 +21,8 @@ size_t dense_partials_bytes(DenseForm form, int64_t M, int64_t N, int64_t K);
 hipError_t launch_dense(DenseForm form, const void* A, const void* B, int64_t M, int64_t N, int64_t K, const void* bias,
                         int act, const void* residual, void* u, void* y, float* partials, hipStream_t s);
 // dU = dy act'(u) to `du` (may be null) and the sums of its columns to `dbias` (may be
-// null; `sums`: slope_parts(T) * N float32)
-int64_t slope_parts(int64_t T);
+// null; `sums`: slope_parts(T, N) * N float32)
+int64_t slope_parts(int64_t T, int N);
 hipError_t launch_slope(const void* dy, const void* u, int act, void* du, void* dbias, float* sums, int64_t T, int N,
                         hipStream_t s);
 

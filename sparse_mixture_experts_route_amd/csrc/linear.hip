@@ -45,31 +45,43 @@ __device__ __forceinline__ float sigmoid(float v) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * v));
 }
 
-__device__ __forceinline__ float act_of(float u, int act) {
-  switch (act) {
-    case MOET_ACT_GELU: return gelu_tanh(u);
-    case MOET_ACT_SILU: return u * sigmoid(u);
-    case MOET_ACT_RELU: return fmaxf(u, 0.0f);
-    default: return u;
-  }
+// act(u), and act'(u). GELU: with s = sigmoid(2 z), z = sqrt(2/pi) (u + 0.044715 u^3),
+// the value is u s and the slope s + 2 u s (1 - s) z'.
+template <int ACT>
+__device__ __forceinline__ float act_one(float u) {
+  if constexpr (ACT == MOET_ACT_GELU) return gelu_tanh(u);
+  if constexpr (ACT == MOET_ACT_SILU) return u * sigmoid(u);
+  if constexpr (ACT == MOET_ACT_RELU) return u > 0.0f ? u : u != u ? u : 0.0f;
+  return u;
 }
 
-// act'(u). GELU: with s = sigmoid(2 z), z = sqrt(2/pi) (u + 0.044715 u^3), the
-// value is u s and the slope s + 2 u s (1 - s) z'.
-__device__ __forceinline__ float act_slope(float u, int act) {
-  switch (act) {
-    case MOET_ACT_GELU: {
-      const float c = 2.0f * 0.7978845608028654f, u2 = u * u;
-      const float s = sigmoid(c * u * fmaf(0.044715f, u2, 1.0f));
-      const float d = c * fmaf(3.0f * 0.044715f, u2, 1.0f) * (s * (1.0f - s));  // 0 where s has saturated
-      return s * (1.0f - s) > 0.0f ? fmaf(u, d, s) : s;
-    }
-    case MOET_ACT_SILU: {
-      const float s = sigmoid(u);
-      return s * (1.0f - s) > 0.0f ? fmaf(u * s, 1.0f - s, s) : s;
-    }
-    case MOET_ACT_RELU: return u > 0.0f ? 1.0f : u != u ? u : 0.0f;
-    default: return 1.0f;
+template <int ACT>
+__device__ __forceinline__ float slope_one(float u) {
+  if constexpr (ACT == MOET_ACT_GELU) {
+    const float c = 2.0f * 0.7978845608028654f, u2 = u * u;
+    const float s = sigmoid(c * u * fmaf(0.044715f, u2, 1.0f)), t = s * (1.0f - s);
+    return t > 0.0f ? fmaf(u * t, c * fmaf(3.0f * 0.044715f, u2, 1.0f), s) : s;  // else it has saturated
+  }
+  if constexpr (ACT == MOET_ACT_SILU) {
+    const float s = sigmoid(u), t = s * (1.0f - s);
+    return t > 0.0f ? fmaf(u, t, s) : s;
+  }
+  if constexpr (ACT == MOET_ACT_RELU) return u > 0.0f ? 1.0f : u != u ? u : 0.0f;
+  return 1.0f;
+}
+
+// N values by one branch
+template <int N>
+__device__ __forceinline__ void act_all(float* f, int act) {
+  if (act == MOET_ACT_GELU) {
+#pragma unroll
+    for (int v = 0; v < N; ++v) f[v] = act_one<MOET_ACT_GELU>(f[v]);
+  } else if (act == MOET_ACT_SILU) {
+#pragma unroll
+    for (int v = 0; v < N; ++v) f[v] = act_one<MOET_ACT_SILU>(f[v]);
+  } else if (act == MOET_ACT_RELU) {
+#pragma unroll
+    for (int v = 0; v < N; ++v) f[v] = act_one<MOET_ACT_RELU>(f[v]);
   }
 }
 
@@ -370,10 +382,7 @@ __global__ __launch_bounds__(WM * WN * 64, OCC * WM * WN / 4) void dense_kernel(
             }
             const int at = inside ? (int)(off * 2) : 0x7FFFFFF0;
             if (E.u) __builtin_amdgcn_raw_buffer_store_b128(narrow8(f), rsU, at, 0, 0);
-            if (E.act != MOET_ACT_NONE) {
-#pragma unroll
-              for (int v = 0; v < 8; ++v) f[v] = act_of(f[v], E.act);
-            }
+            act_all<8>(f, E.act);
             if (E.residual) {
               float w[8];
               widen8(res, w);
@@ -507,8 +516,7 @@ __global__ __launch_bounds__(kThinWaves * kWave) void thin_kernel(DenseArgs args
     for (int v = 0; v < 4; ++v) f[v] += w[v];
   }
   if (E.u) *(u32x2*)(E.u + off) = u32x2{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])};
-#pragma unroll
-  for (int v = 0; v < 4; ++v) f[v] = act_of(f[v], E.act);
+  act_all<4>(f, E.act);
   if (E.residual) {
     widen4(E.residual + off, w);
 #pragma unroll
@@ -542,8 +550,7 @@ __global__ __launch_bounds__(256) void dense_join_kernel(const float* __restrict
       for (int v = 0; v < 8; ++v) f[v] += b[v];
     }
     if (E.u) *(u32x4*)(E.u + off) = narrow8(f);
-#pragma unroll
-    for (int v = 0; v < 8; ++v) f[v] = act_of(f[v], E.act);
+    act_all<8>(f, E.act);
     if (E.residual) {
       float w[8];
       widen8(*(const u32x4*)(E.residual + off), w);
@@ -554,12 +561,15 @@ __global__ __launch_bounds__(256) void dense_join_kernel(const float* __restrict
   }
 }
 
-// dU = dy act'(u), and sums of its columns: 256 columns by `rows` rows a workgroup,
-// 8 columns a thread and 8 rows side by side
-constexpr int kSlopeCols = 256, kSlopeRows = 64;
+// dU = dy act'(u), and sums of its columns: 256 columns by `rows` rows a workgroup, 8
+// columns a thread and 8 rows beside each other. 8192 x 8192: 102 us for 403 MB, behind a
+// product whose 268 MB of results leave the last-level cache meanwhile (2048 columns a
+// workgroup, 4 KB of a row at a time: 106).
+constexpr int kSlopeCols = 256;
+template <int ACT>
 __global__ __launch_bounds__(256) void slope_kernel(const bf16_bits* __restrict__ dy, const bf16_bits* __restrict__ u,
-                                                    int act, bf16_bits* __restrict__ du, float* __restrict__ sums,
-                                                    int64_t T, int N, int64_t rows) {
+                                                    bf16_bits* __restrict__ du, float* __restrict__ sums, int64_t T, int N,
+                                                    int64_t rows) {
   __shared__ float s_v[8][kSlopeCols];
   const int c = threadIdx.x % 32, r0 = threadIdx.x / 32, col = blockIdx.x * kSlopeCols + c * 8;
   const int64_t t0 = (int64_t)blockIdx.y * rows, t1 = min(T, t0 + rows);
@@ -569,11 +579,11 @@ __global__ __launch_bounds__(256) void slope_kernel(const bf16_bits* __restrict_
     for (int64_t t = t0 + r0; t < t1; t += 8) {
       float g[8];
       widen8(*(const u32x4*)(dy + t * N + col), g);
-      if (act != MOET_ACT_NONE) {
+      if constexpr (ACT != MOET_ACT_NONE) {
         float z[8];
         widen8(*(const u32x4*)(u + t * N + col), z);
 #pragma unroll
-        for (int v = 0; v < 8; ++v) g[v] *= act_slope(z[v], act);
+        for (int v = 0; v < 8; ++v) g[v] *= slope_one<ACT>(z[v]);
       }
       if (du) *(u32x4*)(du + t * N + col) = narrow8(g);
 #pragma unroll
@@ -707,14 +717,22 @@ hipError_t launch_dense(DenseForm form, const void* A, const void* B, int64_t M,
   return hipGetLastError();
 }
 
-int64_t slope_parts(int64_t T) { return min(ceil_div(T, (int64_t)kSlopeRows), (int64_t)256); }
+// Workgroups along the rows: 8 rows each at least, about 2048 of them with those along the
+// columns, and at most 256 sums of a column
+int64_t slope_parts(int64_t T, int N) {
+  return max((int64_t)1, min(min(ceil_div(T, (int64_t)8), (int64_t)256), ceil_div((int64_t)2048, ceil_div(N, (int64_t)kSlopeCols))));
+}
 
 hipError_t launch_slope(const void* dy, const void* u, int act, void* du, void* dbias, float* sums, int64_t T, int N,
                         hipStream_t s) {
-  const int64_t parts = slope_parts(T), rows = ceil_div(ceil_div(T, parts), (int64_t)8) * 8;
+  const int64_t parts = slope_parts(T, N), rows = ceil_div(ceil_div(T, parts), (int64_t)8) * 8;
   const int used = (int)ceil_div(T, rows);
-  hipLaunchKernelGGL(slope_kernel, dim3((unsigned)ceil_div(N, kSlopeCols), (unsigned)used), dim3(256), 0, s,
-                     (const bf16_bits*)dy, (const bf16_bits*)u, act, (bf16_bits*)du, dbias ? sums : nullptr, T, N, rows);
+  hipLaunchKernelGGL((act == MOET_ACT_GELU   ? slope_kernel<MOET_ACT_GELU>
+                      : act == MOET_ACT_SILU ? slope_kernel<MOET_ACT_SILU>
+                      : act == MOET_ACT_RELU ? slope_kernel<MOET_ACT_RELU>
+                                             : slope_kernel<MOET_ACT_NONE>),
+                     dim3((unsigned)ceil_div(N, kSlopeCols), (unsigned)used), dim3(256), 0, s, (const bf16_bits*)dy,
+                     (const bf16_bits*)u, (bf16_bits*)du, dbias ? sums : nullptr, T, N, rows);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !dbias) return e;
   hipLaunchKernelGGL(dbias_kernel, dim3((unsigned)(N / 16)), dim3(256), 0, s, (const float*)sums, (bf16_bits*)dbias, used, N);

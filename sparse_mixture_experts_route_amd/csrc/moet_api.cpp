@@ -27,7 +27,7 @@ struct LinearBwdWs {
 LinearBwdWs carve_linear_backward(Carver& c, const moe_problem_t& p) {
   LinearBwdWs w;
   w.du = c.take<uint16_t>((size_t)p.T * p.d_expert);
-  w.sums = c.take<float>((size_t)slope_parts(p.T) * p.d_expert);
+  w.sums = c.take<float>((size_t)slope_parts(p.T, p.d_expert) * p.d_expert);
   w.partials = carve_partials(c, std::max(dense_partials_bytes(DENSE_NT, p.T, p.d_model, p.d_expert),
                                           dense_partials_bytes(DENSE_TN, p.d_model, p.d_expert, p.T)));
   return w;

@@ -37,26 +37,34 @@ namespace {
 
 constexpr int kTB = kPermuteTokensPerBlock;  // tokens per block, one thread each
 constexpr int kWords = kTB / 32;             // mask words per expert
+constexpr int kPitch = kWords + 1;           // of them in LDS: lanes with different experts take different banks
 
 // REPEATS: a token may name an expert twice. `extra[e]` then counts the selections
 // that a mask has no bit for, and the result says whether the block has any.
 template <bool REPEATS = false>
 __device__ __forceinline__ bool build_mask(const int32_t* __restrict__ idx, int64_t T, int k, int E,
-                                           uint32_t (*mask)[kWords], int64_t t0, int* extra = nullptr) {
+                                           uint32_t (*mask)[kPitch], int64_t t0, int* extra = nullptr) {
   uint32_t* flat = &mask[0][0];
-  for (int i = threadIdx.x; i < E * kWords; i += kTB) flat[i] = 0u;
+  for (int i = threadIdx.x; i < E * kPitch; i += kTB) flat[i] = 0u;
   if (REPEATS && (int)threadIdx.x < E) extra[threadIdx.x] = 0;
   __syncthreads();
   const int64_t t = t0 + threadIdx.x;
   bool again = false;
   if (t < T) {
-    for (int j = 0; j < k; ++j) {
-      const int e = idx[t * k + j];
-      if ((unsigned)e < (unsigned)E) {
-        const uint32_t bit = 1u << (threadIdx.x & 31);
-        if (atomicOr(&mask[e][threadIdx.x >> 5], bit) & bit) {
+    const uint32_t bit = 1u << (threadIdx.x & 31);
+    for (int j0 = 0; j0 < k; j0 += 8) {  // eight loads in flight
+      int ev[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) ev[u] = j0 + u < k ? idx[t * k + j0 + u] : -1;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int e = ev[u];
+        if ((unsigned)e >= (unsigned)E) continue;
+        if (!REPEATS) {
+          atomicOr(&mask[e][threadIdx.x >> 5], bit);
+        } else if (atomicOr(&mask[e][threadIdx.x >> 5], bit) & bit) {
           again = true;
-          if (REPEATS) atomicAdd(&extra[e], 1);
+          atomicAdd(&extra[e], 1);
         }
       }
     }
@@ -70,7 +78,7 @@ template <bool REPEATS>
 __global__ __launch_bounds__(kTB) void hist_kernel(const int32_t* __restrict__ idx, int64_t T, int k, int E,
                                                    int32_t* __restrict__ blockcounts, int32_t* __restrict__ zero,
                                                    int nzero) {
-  __shared__ uint32_t mask[256][kWords];
+  __shared__ uint32_t mask[256][kPitch];
   __shared__ int extra[REPEATS ? 256 : 1];
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < nzero; i += kTB) zero[i] = 0;
@@ -183,7 +191,7 @@ constexpr int kFusedScanBlocks = 64;
 // levels of the bits below its token, and the token's own earlier ones.
 // (Ranks are added up in inv; a token's entries are its own thread's.)
 __device__ __noinline__ void scatter_repeats(const int32_t* __restrict__ idx, int64_t T, int k, int E, int64_t t,
-                                             uint32_t (*mask)[kWords], const int32_t* s_base,
+                                             uint32_t (*mask)[kPitch], const int32_t* s_base,
                                              int32_t* __restrict__ perm, int32_t* inv) {
   const int w = threadIdx.x >> 5;
   const uint32_t bit = 1u << (threadIdx.x & 31);
@@ -196,7 +204,7 @@ __device__ __noinline__ void scatter_repeats(const int32_t* __restrict__ idx, in
   for (int m = 0;; ++m) {
     __syncthreads();
     uint32_t* flat = &mask[0][0];
-    for (int i = threadIdx.x; i < E * kWords; i += kTB) flat[i] = 0u;
+    for (int i = threadIdx.x; i < E * kPitch; i += kTB) flat[i] = 0u;
     __syncthreads();
     bool more = false;
     for (int j = 0; j < k; ++j) {
@@ -233,8 +241,9 @@ __global__ __launch_bounds__(kTB) void scatter_kernel(const int32_t* __restrict_
                                                       const int32_t* __restrict__ blockcounts, int64_t nb,
                                                       int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
                                                       int32_t* __restrict__ perm, int32_t* __restrict__ inv) {
-  __shared__ uint32_t mask[256][kWords];
+  __shared__ uint32_t mask[256][kPitch];
   __shared__ int32_t s_base[256];
+  __shared__ int32_t s_before[256][kPitch];
   __shared__ int extra[REPEATS ? 256 : 1];
   const int64_t t0 = (int64_t)blockIdx.x * kTB;
   const int e0 = threadIdx.x;  // kTB = 256 threads: one expert slot each
@@ -251,16 +260,16 @@ __global__ __launch_bounds__(kTB) void scatter_kernel(const int32_t* __restrict_
           before += b0 + u < (int64_t)blockIdx.x ? c[u] : 0;
         }
       }
-    // inclusive Hillis-Steele scan of the totals over the 256 expert slots
-    s_base[e0] = tot;
-    __syncthreads();
-    for (int o = 1; o < 256; o <<= 1) {
-      const int32_t v = e0 >= o ? s_base[e0 - o] : 0;
-      __syncthreads();
-      s_base[e0] += v;
-      __syncthreads();
+    // inclusive scan of the totals over the 256 expert slots: within waves, then over the four
+    int incl = tot;
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+      const int v = __shfl_up(incl, o, kWave);
+      if (e0 % kWave >= o) incl += v;
     }
-    const int32_t incl = s_base[e0];
+    if (e0 % kWave == kWave - 1) s_base[e0 / kWave] = incl;
+    __syncthreads();
+    for (int w = 0; w < e0 / kWave; ++w) incl += s_base[w];
     if (blockIdx.x == 0 && e0 < E) {
       counts[e0] = tot;
       offsets[e0] = incl - tot;
@@ -278,6 +287,16 @@ __global__ __launch_bounds__(kTB) void scatter_kernel(const int32_t* __restrict_
     scatter_repeats(idx, T, k, E, t, mask, s_base, perm, inv);
     return;
   }
+  // tokens of each expert in the words before each
+  if (e0 < E) {
+    int n = 0;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+      s_before[e0][w] = n;
+      n += __popc(mask[e0][w]);
+    }
+  }
+  __syncthreads();
   if (t >= T) return;
   const int w = threadIdx.x >> 5;
   const uint32_t below = (1u << (threadIdx.x & 31)) - 1u;
@@ -292,9 +311,7 @@ __global__ __launch_bounds__(kTB) void scatter_kernel(const int32_t* __restrict_
         const int e = ev[u];
         int32_t r = -1;
         if ((unsigned)e < (unsigned)E) {
-          int rank = __popc(mask[e][w] & below);
-          for (int w2 = 0; w2 < w; ++w2) rank += __popc(mask[e][w2]);
-          r = s_base[e] + rank;
+          r = s_base[e] + s_before[e][w] + __popc(mask[e][w] & below);
           perm[r] = (int32_t)t;
         }
         inv[t * k + j0 + u] = r;

@@ -79,6 +79,23 @@ __device__ __forceinline__ void selections(const int32_t* __restrict__ inv, cons
   }
 }
 
+// A value (int or float) of another lane of the DPP row, and of a given lane
+template <int CTRL, typename V>
+__device__ __forceinline__ V dpp_row(V v) {
+  return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+
+// Sum over the wave: within rows of 16 lanes by DPP, then the four rows' by scalar reads
+template <typename V>
+__device__ __forceinline__ V wave_total(V v) {
+  v += dpp_row<0xB1>(v);   // quad_perm 1, 0, 3, 2
+  v += dpp_row<0x4E>(v);   // quad_perm 2, 3, 0, 1
+  v += dpp_row<0x141>(v);  // row_half_mirror
+  v += dpp_row<0x140>(v);  // row_mirror
+  auto row = [&](int l) { return __builtin_bit_cast(V, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l)); };
+  return (row(0) + row(16)) + (row(32) + row(48));
+}
+
 // Adds the waves' sums of one token and stores them. `slots` [waves][8]; every
 // wave of the workgroup comes here.
 template <int WPT>
@@ -86,7 +103,7 @@ __device__ __forceinline__ void store_dots(float* dot, float* __restrict__ dw, i
                                            float (*slots)[kGroup]) {
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
 #pragma unroll
-  for (int j = 0; j < kGroup; ++j) dot[j] = wave_sum(dot[j]);
+  for (int j = 0; j < kGroup; ++j) dot[j] = wave_total(dot[j]);
   if constexpr (WPT > 1) {
     __syncthreads();  // the slots' last readers are through
 #pragma unroll
@@ -340,16 +357,15 @@ __global__ __launch_bounds__(kThreads) void dispatch_small_kernel(const int32_t*
       e[j] = j0 + j < k ? idx[t * k + j0 + j] : -1;
       n[j] = 0;
     }
-    for (int i = tid; i < P; i += kThreads) {
-      const int f = idx[i];
-      if ((unsigned)f >= (unsigned)E) continue;
+    for (int i0 = 0; i0 < P; i0 += kThreads) {
+      const int i = i0 + tid, f = i < P ? idx[i] : -1;
+      const bool named = (unsigned)f < (unsigned)E;
 #pragma unroll
-      for (int j = 0; j < kGroup; ++j) n[j] += f < e[j] || (f == e[j] && i < t * k + j0 + j);
+      for (int j = 0; j < kGroup; ++j) n[j] += named && (f < e[j] || (f == e[j] && i < t * k + j0 + j));
     }
 #pragma unroll
     for (int j = 0; j < kGroup; ++j) {
-#pragma unroll
-      for (int o = 32; o > 0; o >>= 1) n[j] += __shfl_xor(n[j], o, kWave);
+      n[j] = wave_total(n[j]);
       if (lane == 0) s_row[wave][j] = n[j];
     }
     __syncthreads();
