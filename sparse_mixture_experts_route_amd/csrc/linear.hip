@@ -19,7 +19,10 @@
 // neighbouring columns of a row. Steps of 64 along K through a ring of LDS
 // stages, one barrier a step; reads of the next fragments and the loads of a
 // later stage are issued between the matrix instructions. Workgroups are
-// persistent: while a tile's results leave, the first stages of the next come in.
+// persistent: while a tile's results leave, the first stages of the next come in, and
+// its first step waits for neither (waiting for the stores there: 8192 x 2048 -> 8192
+// 331 us with u, 287 and 269 for the gradients, now 291, 234 and 235: 944 to 1175 TFLOP/s
+// where torch's products reach 1266, 1201 and 970).
 // The results go through LDS of their own as float32 rows, so that bias, activation and
 // residual are applied in 16-byte pieces of the row and rounded once.
 //
@@ -259,6 +262,7 @@ __global__ __launch_bounds__(WM * WN * 64, OCC * WM * WN / 4) void dense_kernel(
     const int kn = it.kn;
     // the stages that were asked for before the last results left; their stores may still be under way
     if (first || args.splits > 1) wait_vmem<0>();
+    else if (args.ep.u) wait_vmem<(2 * STORES < 63 ? 2 * STORES : 63)>();
     else wait_vmem<(STORES < 63 ? STORES : 63)>();
     first = false;
     __syncthreads();
@@ -293,9 +297,11 @@ __global__ __launch_bounds__(WM * WN * 64, OCC * WM * WN / 4) void dense_kernel(
       const bool more = kt + 1 < kn, refill = kt + S < kn;
       const int nbuf = buf + 1 == S ? 0 : buf + 1;
       if (more) {
-        // stage kt + 1 has landed; kt + 2 .. kt + S - 1 may be under way
-        if (kt + S - 1 < kn) wait_vmem<NL * (S - 2)>();
-        else wait_vmem<0>();
+        // stage kt + 1 has landed (the item began with its first S); kt + 2 .. kt + S - 1 may be under way
+        if (kt + 1 >= S) {
+          if (kt + S - 1 < kn) wait_vmem<NL * (S - 2)>();
+          else wait_vmem<0>();
+        }
         __syncthreads();  // every wave's part of it; and all have read `buf`
       }
       constexpr int PER = (NL + NR + (NM - H) - 1) / (NM - H);
@@ -623,11 +629,12 @@ __global__ __launch_bounds__(256) void dbias_kernel(const float* __restrict__ su
 
 }  // namespace
 
-// The tile and the cut along K by estimated time, us, fitted to 16 shapes in three forms
-// (rows 1 to 8192, widths 64 to 8192; within 15% of what they take, and of the best
-// choice). Measured for x W, best of each tile: 32 rows of 2048 to 8192 21 / 16.4 / 12.4,
-// 512 of 2048 to 2048 29.7 / 23.8 / 31.9, 2048 of 2048 to 2048 51 / 39.8 / over 100, 8192 of 2048
-// to 8192 265 / 303 / -.
+// The tile and the cut along K by estimated time, us, fitted to 17 shapes in three forms
+// (rows 1 to 8192, widths 512 to 8192); what it takes is within 10% of the best of each.
+// Measured in a graph on inputs that change, best cut of tile 0 / 1 / 2, x W with bias and
+// GELU: 32 rows of 2048 to 8192 18.5 / 16.4 / 12.6, 256 of 2048 to 2048 26.9 / 16.7 / 18.1,
+// 512 of 2048 to 2048 29.4 / 22.2 / 31.2, 2048 of 2048 to 2048 45.3 / 36.5 / -, 8192 of 2048 to
+// 8192 255 / 276 / -.
 DensePlan dense_plan(DenseForm form, int64_t M, int64_t N, int64_t K) {
   static const int edge[3] = {256, 128, kThin};
   const int cus = device_cus() / 8 * 8;
@@ -645,13 +652,13 @@ DensePlan dense_plan(DenseForm form, int64_t M, int64_t N, int64_t K) {
       if (items >= (int64_t)1 << 22) continue;  // less than 2^32 threads, 8 for each a multiple
       if (fs && fs[0] && splits > 1 && splits > atoi(fs)) continue;
       double us, base;
-      if (tile == 0) base = 5.0, us = ceil_div(items, (int64_t)cus) * steps * 2.05;
+      if (tile == 0) base = 5.0, us = ceil_div(items, (int64_t)cus) * steps * 1.8;
       else if (tile == 1)
-        base = 4.0, us = steps * (items <= cus ? 0.75 + 0.33 * items / cus : ceil_div(items, (int64_t)2 * cus) * 1.25);
+        base = 4.0, us = steps * (items <= cus ? 0.7 + 0.25 * items / cus : ceil_div(items, (int64_t)2 * cus) * 1.2);
       else
         base = 3.0, us = max(1.0, (double)items / cus) * steps * (form == DENSE_NN ? 0.22 : form == DENSE_NT ? 0.18 : 0.25);
       us = base + max(us, 2.0 * (M * K + K * N) / 4.2e6);  // the operands have to come in
-      if (splits > 1) us += 3.0 + 8.0 * M * N * splits / 5.5e6;  // partial sums out and in, and their launch
+      if (splits > 1) us += (tile == 2 ? 3.5 : 3.0) + 8.0 * M * N * splits / 5.5e6;  // partial sums out and in, and their launch
       if (fs && fs[0]) us = -(double)splits;
       if (us < best_us) {
         best_us = us;
