@@ -161,7 +161,7 @@ typedef struct {
  *   counter  [2] int32: steps taken, and 0, which the call uses. It is advanced by one
  *   lr_scale [1] float32 or NULL: a factor of lr that may change between replays of a captured step
  *   grad_scale [1] float32 or NULL; when it is NaN the step is left out: nothing is written
- * Lists of more than 40 tensors take a launch for every 40. MOE_ERR_UNSUPPORTED when
+ * Lists of more than 48 tensors take a launch for every 48. MOE_ERR_UNSUPPORTED when
  * the list reaches 2^41 values. */
 moe_status_t moet_adamw(const moet_tensor_t* tensors, int32_t count, const moet_adamw_t* opt, int32_t* counter,
                         const float* lr_scale, const float* grad_scale, void* stream);
@@ -174,6 +174,12 @@ moe_status_t moet_adamw(const moet_tensor_t* tensors, int32_t count, const moet_
  *   ws  MOET_GRAD_NORM_WS_BYTES */
 moe_status_t moet_grad_norm(const moet_tensor_t* tensors, int32_t count, double max_norm, float* norm, float* scale,
                             void* ws, size_t ws_bytes, void* stream);
+
+/* Both in one call and with a launch less: moet_grad_norm, and moet_adamw with its
+ * scale; norm and scale [1] float32 are written, scale may be NULL. */
+moe_status_t moet_adamw_clipped(const moet_tensor_t* tensors, int32_t count, const moet_adamw_t* opt, int32_t* counter,
+                                const float* lr_scale, double max_norm, float* norm, float* scale, void* ws,
+                                size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -67,6 +67,7 @@ from ._train import (  # noqa: F401
     AdamWOptions,
     Tensor,
     moet_adamw,
+    moet_adamw_clipped,
     moet_combine,
     moet_combine_backward,
     moet_dispatch,

@@ -58,6 +58,7 @@ def _declare():
         "moet_linear": [P, vp, vp, vp, i32, vp, vp, vp, vp, sz, vp],
         "moet_linear_backward": [P, vp, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp],
         "moet_adamw": [A, i32, O, vp, vp, vp, vp],
+        "moet_adamw_clipped": [A, i32, O, vp, vp, f64, vp, vp, vp, sz, vp],
         "moet_grad_norm": [A, i32, f64, vp, vp, vp, sz, vp],
     }
     for name, args in sigs.items():
@@ -190,4 +191,12 @@ def moet_grad_norm(tensors, max_norm, norm, scale, ws, stream=None):
     dev = _device("norm", norm)
     arr, count = _list(tensors)
     _call(_c.moet_grad_norm, dev, stream, arr, count, max_norm, _ptr("norm", norm, 1, _F32, dev),
+          _opt("scale", scale, 1, _F32, dev), *_ws(ws, dev))
+
+
+def moet_adamw_clipped(tensors, opt: AdamWOptions, counter, lr_scale, max_norm, norm, scale, ws, stream=None):
+    dev = _device("counter", counter)
+    arr, count = _list(tensors)
+    _call(_c.moet_adamw_clipped, dev, stream, arr, count, ctypes.byref(opt), _ptr("counter", counter, 2, _I32, dev),
+          _opt("lr_scale", lr_scale, 1, _F32, dev), max_norm, _ptr("norm", norm, 1, _F32, dev),
           _opt("scale", scale, 1, _F32, dev), *_ws(ws, dev))

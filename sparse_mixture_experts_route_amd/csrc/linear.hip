@@ -644,8 +644,9 @@ DensePlan dense_plan(DenseForm form, int64_t M, int64_t N, int64_t K) {
   const int64_t most = max((int64_t)1, nk / 4);  // at least four steps of a cut tile
   DensePlan best{};
   double best_us = 1e30;
-  for (int tile = 0; tile < 3; ++tile) {
-    if (ft && ft[0] && atoi(ft) != tile) continue;
+  for (int i = 0; i < 6 && (i < 3 || best.grid == 0); ++i) {
+    const int tile = i % 3;  // all of them again only where a forced one is not possible
+    if (i < 3 && ft && ft[0] && atoi(ft) != tile) continue;
     const int64_t mt = ceil_div(M, (int64_t)edge[tile]), nt = ceil_div(N, (int64_t)edge[tile]);
     for (int64_t splits = 1; splits <= 32 && splits <= most; splits *= 2) {
       const int64_t items = mt * nt * splits, steps = ceil_div(nk, splits);

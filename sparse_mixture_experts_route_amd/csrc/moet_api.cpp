@@ -243,8 +243,11 @@ int64_t list_values(const moet_tensor_t* t, int32_t count) {
 
 }  // namespace
 
-MOE_API moe_status_t moet_adamw(const moet_tensor_t* tensors, int32_t count, const moet_adamw_t* opt, int32_t* counter,
-                                const float* lr_scale, const float* grad_scale, void* stream) {
+namespace {
+
+// The checks of a step, spans of its tensors included
+moe_status_t check_step(const moet_tensor_t* tensors, int32_t count, const moet_adamw_t* opt, const int32_t* counter,
+                        const float* lr_scale, Spans& spans) {
   if (!opt || !counter) return MOE_ERR_INVALID_ARGUMENT;
   const double b1 = opt->beta1, b2 = opt->beta2;
   if (!std::isfinite(opt->lr) || opt->lr < 0 || !(b1 >= 0 && b1 < 1) || !(b2 >= 0 && b2 < 1) ||
@@ -253,29 +256,24 @@ MOE_API moe_status_t moet_adamw(const moet_tensor_t* tensors, int32_t count, con
   const int64_t total = list_values(tensors, count);
   if (total == -1) return MOE_ERR_INVALID_ARGUMENT;
   if (total == -2) return MOE_ERR_UNSUPPORTED;
-  Spans spans;
-  bool ok = spans.add(counter, 8, true) && (!lr_scale || spans.add(lr_scale, 4, false)) &&
-            (!grad_scale || spans.add(grad_scale, 4, false));
+  bool ok = spans.add(counter, 8, true) && (!lr_scale || spans.add(lr_scale, 4, false));
   for (int i = 0; ok && i < count; ++i) {
     const moet_tensor_t& t = tensors[i];
+    if (!t.n) continue;
     if (!dtype_ok(t.param_dtype) || !std::isfinite(t.lr_factor) || t.lr_factor < 0 || !std::isfinite(t.weight_decay) ||
         t.weight_decay < 0 || (t.param_dtype == MOE_DTYPE_BF16) != !!t.master || !!t.m_scale != !!t.v_scale)
-      if (t.n) return MOE_ERR_INVALID_ARGUMENT;
-    if (!t.n) continue;
+      return MOE_ERR_INVALID_ARGUMENT;
     const size_t n = (size_t)t.n, blocks = (n + 127) / 128, mb = t.m_scale ? n : 4 * n;
     ok = spans.add(t.param, n * elem_size(t.param_dtype), true) && spans.add(t.grad, n * elem_size(t.grad_dtype), false) &&
          (!t.master || spans.add(t.master, 4 * n, true)) && spans.add(t.m, mb, true) && spans.add(t.v, mb, true) &&
          (!t.m_scale || (spans.add(t.m_scale, blocks, true) && spans.add(t.v_scale, blocks, true)));
   }
-  if (!ok || !spans.apart()) return MOE_ERR_INVALID_ARGUMENT;
-  OptHyper h;
-  h.lr = opt->lr;
-  h.beta1 = b1;
-  h.beta2 = b2;
-  h.log_beta1 = std::log(b1);
-  h.log_beta2 = std::log(b2);
-  h.eps = (float)opt->eps;
-  h.seed = opt->seed;
+  return ok ? MOE_OK : MOE_ERR_INVALID_ARGUMENT;
+}
+
+moe_status_t run_step(const moet_tensor_t* tensors, int32_t count, const moet_adamw_t* opt, int32_t* counter,
+                      const float* lr_scale, const GradScale& gs, hipStream_t s) {
+  const OptHyper h = {opt->lr, opt->beta1, opt->beta2, std::log(opt->beta1), std::log(opt->beta2), (float)opt->eps, opt->seed};
   OptList l;
   int i = 0;
   do {
@@ -284,18 +282,48 @@ MOE_API moe_status_t moet_adamw(const moet_tensor_t* tensors, int32_t count, con
     l.base = i;
     for (; i < count && l.count < kOptTensors; ++i) {
       const moet_tensor_t& t = tensors[i];
-      OptTensor& d = l.t[l.count++];
-      d = {t.param, t.grad, t.master, t.m, t.v, (uint8_t*)t.m_scale, (uint8_t*)t.v_scale, t.n, (float)t.lr_factor,
-           (float)t.weight_decay,
-           (t.grad_dtype == MOE_DTYPE_BF16 ? kGrad16 : 0u) | (t.master ? kParam16 : 0u) | (t.m_scale ? kMoments8 : 0u),
-           l.chunks};
+      l.t[l.count++] = {t.param, t.grad, t.master, t.m, t.v, (uint8_t*)t.m_scale, (uint8_t*)t.v_scale, t.n,
+                        (float)t.lr_factor, (float)t.weight_decay,
+                        (t.grad_dtype == MOE_DTYPE_BF16 ? kGrad16 : 0u) | (t.master ? kParam16 : 0u) |
+                            (t.m_scale ? kMoments8 : 0u),
+                        l.chunks};
       l.chunks += (int32_t)((t.n + kOptChunk - 1) / kOptChunk);
     }
     l.last = i >= count;
-    const hipError_t e = launch_adamw(l, h, counter, lr_scale, grad_scale, (hipStream_t)stream);
-    if (e != hipSuccess) return MOE_ERR_HIP;
+    if (launch_adamw(l, h, counter, lr_scale, gs, s) != hipSuccess) return MOE_ERR_HIP;
   } while (i < count);
   return MOE_OK;
+}
+
+// Sums of squares of a list's gradients, to slots in ws
+moe_status_t run_squares(const moet_tensor_t* tensors, int32_t count, double* slots, hipStream_t s) {
+  NormList l;
+  int i = 0;
+  do {
+    l.count = 0;
+    l.chunks = 0;
+    l.add = i > 0;
+    for (; i < count && l.count < kNormTensors; ++i) {
+      const moet_tensor_t& t = tensors[i];
+      l.t[l.count++] = {t.grad, t.n, l.chunks, t.grad_dtype == MOE_DTYPE_BF16 ? 1u : 0u};
+      l.chunks += (int32_t)((t.n + kOptChunk - 1) / kOptChunk);
+    }
+    if (launch_square_sums(l, slots, s) != hipSuccess) return MOE_ERR_HIP;
+  } while (i < count);
+  return MOE_OK;
+}
+
+static_assert(kNormSlots * sizeof(double) + kAlign <= MOET_GRAD_NORM_WS_BYTES, "partial sums");
+
+}  // namespace
+
+MOE_API moe_status_t moet_adamw(const moet_tensor_t* tensors, int32_t count, const moet_adamw_t* opt, int32_t* counter,
+                                const float* lr_scale, const float* grad_scale, void* stream) {
+  Spans spans;
+  const moe_status_t st = check_step(tensors, count, opt, counter, lr_scale, spans);
+  if (st != MOE_OK) return st;
+  if ((grad_scale && !spans.add(grad_scale, 4, false)) || !spans.apart()) return MOE_ERR_INVALID_ARGUMENT;
+  return run_step(tensors, count, opt, counter, lr_scale, {grad_scale, nullptr, 0.0, nullptr, nullptr}, (hipStream_t)stream);
 }
 
 MOE_API moe_status_t moet_grad_norm(const moet_tensor_t* tensors, int32_t count, double max_norm, float* norm,
@@ -311,20 +339,25 @@ MOE_API moe_status_t moet_grad_norm(const moet_tensor_t* tensors, int32_t count,
     ok = !tensors[i].n || spans.add(tensors[i].grad, (size_t)tensors[i].n * elem_size(tensors[i].grad_dtype), false);
   if (!ok || !spans.apart()) return MOE_ERR_INVALID_ARGUMENT;
   if (ws_bytes < MOET_GRAD_NORM_WS_BYTES) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  static_assert(kNormSlots * sizeof(double) + kAlign <= MOET_GRAD_NORM_WS_BYTES, "partial sums");
   double* slots = (double*)align_ws(ws);
-  NormList l;
-  int i = 0;
-  do {
-    l.count = 0;
-    l.chunks = 0;
-    l.add = i > 0;
-    for (; i < count && l.count < kNormTensors; ++i) {
-      const moet_tensor_t& t = tensors[i];
-      l.t[l.count++] = {t.grad, t.n, l.chunks, t.grad_dtype == MOE_DTYPE_BF16 ? 1u : 0u};
-      l.chunks += (int32_t)((t.n + kOptChunk - 1) / kOptChunk);
-    }
-    if (launch_square_sums(l, slots, (hipStream_t)stream) != hipSuccess) return MOE_ERR_HIP;
-  } while (i < count);
+  const moe_status_t st = run_squares(tensors, count, slots, (hipStream_t)stream);
+  if (st != MOE_OK) return st;
   return hip_status(launch_norm_scale(slots, max_norm, norm, scale, (hipStream_t)stream));
+}
+
+MOE_API moe_status_t moet_adamw_clipped(const moet_tensor_t* tensors, int32_t count, const moet_adamw_t* opt,
+                                        int32_t* counter, const float* lr_scale, double max_norm, float* norm,
+                                        float* scale, void* ws, size_t ws_bytes, void* stream) {
+  if (!norm || !ws || !(max_norm > 0)) return MOE_ERR_INVALID_ARGUMENT;
+  Spans spans;
+  moe_status_t st = check_step(tensors, count, opt, counter, lr_scale, spans);
+  if (st != MOE_OK) return st;
+  if (!spans.add(norm, 4, true) || (scale && !spans.add(scale, 4, true)) ||
+      !spans.add(ws, MOET_GRAD_NORM_WS_BYTES, true) || !spans.apart())
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (ws_bytes < MOET_GRAD_NORM_WS_BYTES) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  double* slots = (double*)align_ws(ws);
+  st = run_squares(tensors, count, slots, (hipStream_t)stream);
+  if (st != MOE_OK) return st;
+  return run_step(tensors, count, opt, counter, lr_scale, {nullptr, slots, max_norm, norm, scale}, (hipStream_t)stream);
 }

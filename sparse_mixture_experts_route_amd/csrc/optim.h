@@ -9,7 +9,6 @@ namespace moe {
 
 constexpr int kOptThreads = 256;
 constexpr int kOptChunk = 2048;      // values that a workgroup takes at once, 8 a thread
-constexpr int kOptTensors = 40;      // of one launch: the arguments stay below 4 KB
 constexpr int kNormTensors = 128;    // of one launch of the norm
 constexpr int kNormSlots = 1024;     // workgroups, and partial sums, of the norm
 
@@ -26,6 +25,8 @@ struct OptTensor {
   uint32_t flags;
   int32_t first;  // first chunk of the launch
 };
+
+constexpr int kOptTensors = 48;  // of one launch: with the other arguments 4 KB
 
 struct OptList {
   OptTensor t[kOptTensors];
@@ -55,10 +56,19 @@ struct NormList {
   int32_t add;  // 1: onto the partial sums of the launch before
 };
 
-static_assert(sizeof(OptList) + sizeof(OptHyper) + 64 <= 4096 && sizeof(NormList) + 64 <= 4096, "kernel arguments");
+// Where the gradients' factor comes from: `scale` (may be null: 1), or, with `slots`, the
+// sums of squares of launch_square_sums, from which norm and scale are written too
+struct GradScale {
+  const float* scale;
+  const double* slots;
+  double max_norm;
+  float *norm_out, *scale_out;
+};
+
+static_assert(sizeof(OptList) + sizeof(OptHyper) + sizeof(GradScale) + 16 <= 4096 && sizeof(NormList) + 64 <= 4096, "kernel arguments");
 
 hipError_t launch_adamw(const OptList& l, const OptHyper& h, int32_t* counter, const float* lr_scale,
-                        const float* grad_scale, hipStream_t s);
+                        const GradScale& gs, hipStream_t s);
 // One launch over a list; the partial sums in `slots` [kNormSlots]
 hipError_t launch_square_sums(const NormList& l, double* slots, hipStream_t s);
 hipError_t launch_norm_scale(const double* slots, double max_norm, float* norm, float* scale, hipStream_t s);

@@ -11,8 +11,13 @@
 //
 // The moments are updated in 64 bits, where a CU multiplies as fast as in
 // 32: their codes then do not depend on how the two products are rounded.
+//
+// Measured: 67 million values, moments in 32 bits 381 us (4.9 TB/s), in 8 bits 226 us
+// (4.8 TB/s), their norm 28 to 43 us (the step before leaves the last-level cache meanwhile);
+// 525 thousand values in 5 tensors 6.7 us, a step with its norm 11 us.
 #include "common.h"
 #include "e4m3.h"
+#include "internal.h"
 #include "optim.h"
 
 namespace moe {
@@ -235,53 +240,95 @@ __device__ __forceinline__ void update_chunk(const OptTensor& T, const Hyper& h,
 
 template <bool G16, bool P16, bool S8>
 __device__ __forceinline__ void update(const OptTensor& T, const Hyper& h, int64_t first) {
-  const int64_t i0 = first + threadIdx.x * kVals;
+  const int64_t i0 = first + threadIdx.x % kOptThreads * kVals;
   if (first + kOptChunk <= T.n) update_chunk<G16, P16, S8, true>(T, h, i0);
   else update_chunk<G16, P16, S8, false>(T, h, i0);
 }
 
-// Index of the tensor that chunk c is of, not before `from`: the last whose first chunk is not above it
-template <typename L>
-__device__ __forceinline__ int tensor_of(const L& l, int c, int from = 0) {
-  if (from + 1 >= l.count || l.t[from + 1].first > c) return from;
-  int a = from + 1, b = l.count;
-  while (b - a > 1) {
-    const int mid = (a + b) >> 1;
-    if (l.t[mid].first <= c) a = mid;
-    else b = mid;
+// First chunks of a list's tensors, one or two a lane, loaded together; the tensor of chunk
+// c is the last whose first chunk is not above it. (A search through the arguments would
+// wait for each of its steps.)
+template <typename L, int N>
+struct Finder {
+  int first[(N + kWave - 1) / kWave];
+  __device__ __forceinline__ explicit Finder(const L& l) {
+#pragma unroll
+    for (int i = 0; i * kWave < N; ++i) {
+      const int j = i * kWave + threadIdx.x % kWave;
+      first[i] = j < l.count ? l.t[j].first : INT32_MAX;
+    }
   }
-  return a;
+  __device__ __forceinline__ int tensor(int c) const {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i * kWave < N; ++i) n += __popcll(__ballot(first[i] <= c));
+    return n - 1;
+  }
+};
+
+// Sum over a workgroup of N threads, the same order and the same bits in each of them
+template <int N>
+__device__ __forceinline__ double block_sum(double v, double* slots) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
+  if (threadIdx.x % kWave == 0) slots[threadIdx.x / kWave] = v;
+  __syncthreads();
+  v = 0.0;
+#pragma unroll
+  for (int i = 0; i < N / kWave; ++i) v += slots[i];
+  return v;
 }
 
-__global__ __launch_bounds__(kOptThreads) void adamw_kernel(const OptList l, const OptHyper o,
+// The factor that clips gradients of norm n, NaN when it is not finite
+__device__ __forceinline__ float clip_scale(double n, double max_norm) {
+  return n <= max_norm ? 1.0f : n < INFINITY ? (float)(max_norm / n) : NAN;
+}
+
+// Four chunks a workgroup side by side: each workgroup takes part in the count at the end,
+// one after another (259 of them 2.7 us, 65 0.8).
+constexpr int kAdamSide = 4;
+__global__ __launch_bounds__(kAdamSide * kOptThreads) void adamw_kernel(const OptList l, const OptHyper o,
                                                             int32_t* __restrict__ counter,
-                                                            const float* __restrict__ lr_scale,
-                                                            const float* __restrict__ grad_scale) {
+                                                            const float* __restrict__ lr_scale, const GradScale g) {
   const int32_t before = __hip_atomic_load(counter, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  const float gs = grad_scale ? *grad_scale : 1.0f;
+  float gs = g.scale ? *g.scale : 1.0f;
+  const float ls = lr_scale ? *lr_scale : 1.0f;
+  const Finder<OptList, kOptTensors> find(l);
+  if (g.slots) {  // every workgroup adds them for itself: a launch and its wait less
+    static_assert(kNormSlots == kAdamSide * kOptThreads, "a sum for each thread");
+    __shared__ double s_v[kAdamSide * kOptThreads / kWave];
+    const double n = sqrt(block_sum<kAdamSide * kOptThreads>(g.slots[threadIdx.x], s_v));
+    gs = clip_scale(n, g.max_norm);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      g.norm_out[0] = (float)n;
+      if (g.scale_out) g.scale_out[0] = gs;
+    }
+  }
   const bool skip = gs != gs;
   if (!skip) {
+    // 1 - b^t; with b below 1 - 1e-8 the difference is good for float32
     const double t = (double)(before + 1);
-    const double c1 = -expm1(t * o.log_beta1), c2 = -expm1(t * o.log_beta2);
-    const double lr = o.lr * (lr_scale ? (double)*lr_scale : 1.0);
+    const float c1 = (float)(1.0 - exp(t * o.log_beta1)), c2 = (float)(1.0 - exp(t * o.log_beta2));
+    const float lr = (float)(o.lr * (double)ls);
     const uint32_t draw = (uint32_t)(before + 1) * 0x9E3779B9u;
     Hyper h;
     h.b1 = o.beta1;
     h.b2 = o.beta2;
     h.gs = gs;
-    h.root = (float)(1.0 / sqrt(c2));
+    h.root = __builtin_amdgcn_rsqf(c2);
     h.eps = o.eps;
     // Workgroups side by side take neighbouring chunks: ranges of their own, all at the
     // same place of the memory channels' period at a time, took 28% longer for the norm.
-    for (int c = blockIdx.x, j = 0; c < l.chunks; c += gridDim.x) {
-      j = tensor_of(l, c, j);
+    for (int c = __builtin_amdgcn_readfirstlane(blockIdx.x * kAdamSide + threadIdx.x / kOptThreads); c < l.chunks;
+         c += gridDim.x * kAdamSide) {
+      const int j = __builtin_amdgcn_readfirstlane(find.tensor(c));
       const OptTensor& T = l.t[j];
-      const double f = lr * (double)T.lr_factor;
-      h.step = (float)(f / c1);
-      h.decay = (float)(f * (double)T.weight_decay);
+      const float f = lr * T.lr_factor;
+      h.step = f / c1;
+      h.decay = f * T.weight_decay;
       h.key = mix32(o.seed + mix32(draw + (uint32_t)(l.base + j)));
       const int64_t i0 = (int64_t)(c - T.first) * kOptChunk;
-      switch (T.flags) {  // the same for the whole workgroup
+      switch (T.flags) {  // the same for the chunk's waves
         case 0: update<false, false, false>(T, h, i0); break;
         case kGrad16: update<true, false, false>(T, h, i0); break;
         case kParam16: update<false, true, false>(T, h, i0); break;
@@ -307,20 +354,11 @@ __global__ __launch_bounds__(kOptThreads) void adamw_kernel(const OptList l, con
   }
 }
 
-// Sum of 256 threads' values, the same order every time; thread 0 has it
-__device__ __forceinline__ double block_sum(double v, double* slots) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
-  if (threadIdx.x % kWave == 0) slots[threadIdx.x / kWave] = v;
-  __syncthreads();
-  return threadIdx.x == 0 ? (slots[0] + slots[1]) + (slots[2] + slots[3]) : 0.0;
-}
-
 __global__ __launch_bounds__(kOptThreads) void square_sums_kernel(const NormList l, double* __restrict__ slots) {
   __shared__ double s_v[kOptThreads / kWave];
   double sum = 0.0;
   constexpr int U = 4;  // chunks under way together
-  int j = 0;
+  const Finder<NormList, kNormTensors> find(l);
   for (int c0 = blockIdx.x; c0 < l.chunks; c0 += gridDim.x * U) {
     u32x4 q[U][2];
     uint32_t b16[U];
@@ -330,8 +368,7 @@ __global__ __launch_bounds__(kOptThreads) void square_sums_kernel(const NormList
       b16[u] = 0;
       q[u][0] = q[u][1] = u32x4{0u, 0u, 0u, 0u};
       if (c >= l.chunks) continue;
-      j = tensor_of(l, c, j);
-      const NormTensor& T = l.t[j];
+      const NormTensor& T = l.t[__builtin_amdgcn_readfirstlane(find.tensor(c))];
       const int64_t first = (int64_t)(c - T.first) * kOptChunk, i = first + threadIdx.x * kVals;
       b16[u] = T.flags;
       if (first + kOptChunk <= T.n) {
@@ -360,30 +397,29 @@ __global__ __launch_bounds__(kOptThreads) void square_sums_kernel(const NormList
       }
     }
   }
-  sum = block_sum(sum, s_v);
+  sum = block_sum<kOptThreads>(sum, s_v);
   if (threadIdx.x == 0) slots[blockIdx.x] = l.add ? slots[blockIdx.x] + sum : sum;
 }
 
-__global__ __launch_bounds__(kOptThreads) void norm_scale_kernel(const double* __restrict__ slots, double max_norm,
-                                                                 float* __restrict__ norm, float* __restrict__ scale) {
-  __shared__ double s_v[kOptThreads / kWave];
-  double v = 0.0;
-#pragma unroll
-  for (int i = 0; i < kNormSlots / kOptThreads; ++i) v += slots[i * kOptThreads + threadIdx.x];
-  v = block_sum(v, s_v);
+// The sums are added as moet_adamw_clipped's workgroups add them: the same bits
+__global__ __launch_bounds__(kNormSlots) void norm_scale_kernel(const double* __restrict__ slots, double max_norm,
+                                                                float* __restrict__ norm, float* __restrict__ scale) {
+  __shared__ double s_v[kNormSlots / kWave];
+  const double v = slots[threadIdx.x];
+  const double n = sqrt(block_sum<kNormSlots>(v, s_v));
   if (threadIdx.x == 0) {
-    const double n = sqrt(v);
     norm[0] = (float)n;
-    if (scale) scale[0] = n <= max_norm ? 1.0f : n < INFINITY ? (float)(max_norm / n) : NAN;
+    if (scale) scale[0] = clip_scale(n, max_norm);
   }
 }
 
 }  // namespace
 
 hipError_t launch_adamw(const OptList& l, const OptHyper& h, int32_t* counter, const float* lr_scale,
-                        const float* grad_scale, hipStream_t s) {
-  const unsigned grid = (unsigned)max(1, min(l.chunks, 2048));
-  hipLaunchKernelGGL(adamw_kernel, dim3(grid), dim3(kOptThreads), 0, s, l, h, counter, lr_scale, grad_scale);
+                        const GradScale& gs, hipStream_t s) {
+  // a workgroup's 16 waves of up to 128 registers fill a CU
+  const unsigned grid = (unsigned)max(1, min((l.chunks + kAdamSide - 1) / kAdamSide, device_cus()));
+  hipLaunchKernelGGL(adamw_kernel, dim3(grid), dim3(kAdamSide * kOptThreads), 0, s, l, h, counter, lr_scale, gs);
   return hipGetLastError();
 }
 
@@ -393,7 +429,7 @@ hipError_t launch_square_sums(const NormList& l, double* slots, hipStream_t s) {
 }
 
 hipError_t launch_norm_scale(const double* slots, double max_norm, float* norm, float* scale, hipStream_t s) {
-  hipLaunchKernelGGL(norm_scale_kernel, dim3(1), dim3(kOptThreads), 0, s, slots, max_norm, norm, scale);
+  hipLaunchKernelGGL(norm_scale_kernel, dim3(1), dim3(kNormSlots), 0, s, slots, max_norm, norm, scale);
   return hipGetLastError();
 }
 

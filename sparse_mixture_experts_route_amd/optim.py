@@ -1,4 +1,4 @@
-"""AdamW over a list of tensors, on the library's moet_grad_norm and moet_adamw."""
+"""AdamW over a list of tensors, on the library's moet_adamw and moet_adamw_clipped."""
 
 from __future__ import annotations
 
@@ -70,6 +70,8 @@ class AdamW:
                 raise ValueError(f"parameter {i} is on {self.params[i].device}, the first on {self.device}")
             self._list[i] = _train.tensor_entry(self.params[i], None, self.master[i], self.m[i], self.m_scale[i],
                                                 self.v[i], self.v_scale[i], float(f), float(d))
+        self._entries = list(self._list)  # each entry's own view of the array
+        self._options = _train.AdamWOptions()
         with torch.cuda.device(self.device):
             self.lr_scale = torch.ones(1, device=self.device)
             self.norm, self.scale = (torch.ones(1, device=self.device) for _ in range(2))
@@ -116,11 +118,13 @@ class AdamW:
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
         self._keep(stream)
         dev = self.device.index
-        for e, g in zip(self._list, grads):
+        for e, g in zip(self._entries, grads):
             _train.set_grad(e, g, dev)
-        opt = _train.AdamWOptions(self.lr, self.betas[0], self.betas[1], self.eps, self.seed & 0xFFFFFFFF)
-        if self.max_norm is not None:
-            _train.moet_grad_norm(self._list, self.max_norm, self.norm, self.scale, self._ws, stream)
-        _train.moet_adamw(self._list, opt, self.counter, self.lr_scale, self.scale if self.max_norm is not None else None,
-                          stream)
-        return self.norm if self.max_norm is not None else None
+        opt, clip = self._options, self.max_norm is not None
+        opt.lr, (opt.beta1, opt.beta2), opt.eps, opt.seed = self.lr, self.betas, self.eps, self.seed & 0xFFFFFFFF
+        if not clip:
+            _train.moet_adamw(self._list, opt, self.counter, self.lr_scale, None, stream)
+            return None
+        _train.moet_adamw_clipped(self._list, opt, self.counter, self.lr_scale, self.max_norm, self.norm, self.scale, self._ws,
+                                  stream)
+        return self.norm

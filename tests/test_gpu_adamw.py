@@ -136,6 +136,26 @@ def test_clipping(moe, max_norm, clips):
     ref.check(grads, scale=np.float32(scale))
 
 
+def test_clipped_is_norm_and_step(moe):
+    """One call and two give the same bits: norm, factor, parameters and moments, also of long lists."""
+    announce("adamw clipped in one call and in two")
+    params, grads = params_of([(300 + 91 * i, BF if i % 2 else F32, BF) for i in range(140)], 14)
+    other = [p.clone() for p in params]
+    mk = lambda ps: moe.AdamW(ps, lr=LR, bits=[8 if i % 3 else 32 for i in range(140)], max_norm=0.3, seed=2)  # noqa: E731
+    a, b = mk(params), mk(other)
+    a.step(grads)
+    norm, scale = torch.zeros(1, device="cuda"), torch.zeros(1, device="cuda")
+    ws = torch.empty(moe.MOET_GRAD_NORM_WS_BYTES, dtype=torch.uint8, device="cuda")
+    for e, g in zip(b._entries, grads):
+        moe.set_grad(e, g, 0)
+    moe.moet_grad_norm(b._list, 0.3, norm, scale, ws)
+    moe.moet_adamw(b._list, moe.AdamWOptions(LR, 0.9, 0.999, 1e-8, 2), b.counter, None, scale)
+    torch.cuda.synchronize()
+    assert torch.equal(norm, a.norm) and torch.equal(scale, a.scale) and float(scale) < 1
+    for x, y in zip((*params, *a.m, *a.v, a.counter), (*other, *b.m, *b.v, b.counter)):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
 def test_gradients_that_are_not_finite_leave_the_step_out(moe, bad):
     announce(f"adamw skips {bad}")

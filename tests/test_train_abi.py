@@ -24,7 +24,7 @@ def declared():
 def test_header_and_library_agree(libmoe_path):
     out = subprocess.run(["nm", "-D", "--defined-only", libmoe_path], capture_output=True, text=True).stdout
     assert sorted(set(re.findall(r"\bT (moet_\w+)", out))) == declared()
-    assert len(declared()) == 10
+    assert len(declared()) == 11
 
 
 @pytest.fixture(scope="module")
@@ -196,6 +196,22 @@ def test_adamw_refuses(moe, lib):
     assert adamw_status(moe, lib, [entry(moe, small=True, v_scale=at(5))]) == INVALID
     assert adamw_status(moe, lib, [one], lr_scale=at(0)) == INVALID
     assert adamw_status(moe, lib, [one], grad_scale=at(1000)) == INVALID
+
+
+def test_clipped_step_refuses(moe, lib):
+    one, ws, ok = arr(moe, entry(moe)), at(300), moe.MOET_GRAD_NORM_WS_BYTES
+    o = ctypes.byref(moe.AdamWOptions(1e-3, 0.9, 0.99, 1e-8, 1))
+    f = lambda *a: lib.moet_adamw_clipped(*a, None)  # noqa: E731
+    d = ctypes.c_double
+    for bad in (0.0, -1.0, float("nan")):
+        assert f(one, 1, o, at(1000), None, d(bad), at(301), at(302), ws, ok) == INVALID
+    for a in ((None, 1, o, at(1000), None, d(1), at(301), at(302), ws, ok), (one, 1, None, at(1000), None, d(1), at(301), None, ws, ok),
+              (one, 1, o, None, None, d(1), at(301), None, ws, ok), (one, 1, o, at(1000), None, d(1), None, None, ws, ok),
+              (one, 1, o, at(1000), None, d(1), at(301), None, None, ok), (one, 1, o, at(1000), None, d(1), at(301), at(301), ws, ok),
+              (one, 1, o, at(1000), None, d(1), at(1000), None, ws, ok), (one, 1, o, at(1000), at(301), d(1), at(301), None, ws, ok),
+              (one, 1, o, at(1000), None, d(1), at(1), None, ws, ok), (one, 1, o, at(1000), None, d(1), at(301), None, at(3), ok)):
+        assert f(*a) == INVALID
+    assert f(one, 1, o, at(1000), None, d(1), at(301), None, ws, ok - 1) == WS_SMALL
 
 
 def test_grad_norm_refuses(moe, lib):

@@ -54,6 +54,7 @@ for got, want in (
     (lib.moet_linear_backward(p, a[0], a[1], a[2], 1, a[3], a[4], a[5], a[6], a[7], small, None), 3),
     (lib.moet_adamw(full(1, None), 1, o, at(99999), None, None, None), 1),
     (lib.moet_adamw(full(1024, at(1).value), 1024, o, at(99999), None, None, None), 1),
+    (lib.moet_adamw_clipped(full(1024, at(1).value), 1024, o, at(99999), None, ctypes.c_double(1), at(99998), None, at(99997), small, None), 1),
     (lib.moet_grad_norm(full(1024, None), 1024, ctypes.c_double(1), at(99999), at(99998), at(99997), small, None), 3),
 ):
     assert got == want, (got, want)
