@@ -21,8 +21,10 @@
 // later stage are issued between the matrix instructions. Workgroups are
 // persistent: while a tile's results leave, the first stages of the next come in, and
 // its first step waits for neither (waiting for the stores there: 8192 x 2048 -> 8192
-// 331 us with u, 287 and 269 for the gradients, now 291, 234 and 235: 944 to 1175 TFLOP/s
-// where torch's products reach 1266, 1201 and 970).
+// 331 us with u, 287 and 269 for the gradients, then 291, 234 and 235; now 271, 225 and
+// 230: 1014 to 1222 TFLOP/s where torch's products alone reach 1215, 1153 and 943. Other
+// places of the barrier, of the reads and of the loads among the matrix instructions, and
+// priorities, make no difference).
 // The results go through LDS of their own as float32 rows, so that bias, activation and
 // residual are applied in 16-byte pieces of the row and rounded once.
 //
@@ -367,7 +369,7 @@ __global__ __launch_bounds__(WM * WN * 64, OCC * WM * WN / 4) void dense_kernel(
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             const int row = lane & 31, ch = v * 2 + (lane >> 5);
-            *(__attribute__((address_space(3))) f32x4*)(ep + row * 128 + ((ch ^ (row & 7)) << 4)) =
+            *(__attribute__((address_space(3))) f32x4*)(ep + row * 128 + ((ch ^ ((row >> 1) & 7)) << 4)) =
                 f32x4{acc[a][b][4 * v], acc[a][b][4 * v + 1], acc[a][b][4 * v + 2], acc[a][b][4 * v + 3]};
           }
           // a wave's LDS operations are done in their order
@@ -382,12 +384,14 @@ __global__ __launch_bounds__(WM * WN * 64, OCC * WM * WN / 4) void dense_kernel(
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
               const f32x4 w = *(__attribute__((address_space(3))) f32x4*)(
-                  ep + r * 128 + ((((lane % 4) * 2 + v) ^ (r & 7)) << 4));
+                  ep + r * 128 + ((((lane % 4) * 2 + v) ^ ((r >> 1) & 7)) << 4));
 #pragma unroll
               for (int z = 0; z < 4; ++z) f[4 * v + z] = w[z] + bias[4 * v + z];
             }
             const int at = inside ? (int)(off * 2) : 0x7FFFFFF0;
-            if (E.u) __builtin_amdgcn_raw_buffer_store_b128(narrow8(f), rsU, at, 0, 0);
+            // u passes by the caches: the backward pass reads it, later than they keep it
+            // (8192 x 2048 -> 8192 with u 296 -> 271 us)
+            if (E.u) __builtin_amdgcn_raw_buffer_store_b128(narrow8(f), rsU, at, 0, 2);
             act_all<8>(f, E.act);
             if (E.residual) {
               float w[8];
