@@ -588,10 +588,10 @@ __global__ __launch_bounds__(256) void slope_kernel(const bf16_bits* __restrict_
 #pragma unroll 4
     for (int64_t t = t0 + r0; t < t1; t += 8) {
       float g[8];
-      widen8(*(const u32x4*)(dy + t * N + col), g);
+      widen8(__builtin_nontemporal_load((const u32x4*)(dy + t * N + col)), g);
       if constexpr (ACT != MOET_ACT_NONE) {
         float z[8];
-        widen8(*(const u32x4*)(u + t * N + col), z);
+        widen8(__builtin_nontemporal_load((const u32x4*)(u + t * N + col)), z);
 #pragma unroll
         for (int v = 0; v < 8; ++v) g[v] *= slope_one<ACT>(z[v]);
       }
