@@ -12,8 +12,8 @@
 // The moments are updated in 64 bits, where a CU multiplies as fast as in
 // 32: their codes then do not depend on how the two products are rounded.
 //
-// Measured: 67 million values, moments in 32 bits 381 us (4.9 TB/s), in 8 bits 226 us
-// (4.8 TB/s), their norm 28 to 43 us (the step before leaves the last-level cache meanwhile);
+// Measured: 67 million values, moments in 32 bits 358 us (5.2 TB/s), in 8 bits 205 us
+// (5.2 TB/s), their norm 28 us;
 // 525 thousand values in 5 tensors 6.7 us, a step with its norm 11 us.
 #include "common.h"
 #include "e4m3.h"
@@ -34,8 +34,22 @@ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
   return x ^ (x >> 16);
 }
 
+// NT: a long list's master copies and moments pass by the caches, which would not keep
+// them until the next step (67 million values, 32-bit moments with the norm 408 -> 385 us, 8-bit
+// 256 -> 234; 3.6 million in 48 tensors, the same ones again, 24.7 -> 26.0)
+template <bool NT, typename V>
+__device__ __forceinline__ V load(const V* p) {
+  return NT ? __builtin_nontemporal_load(p) : *p;
+}
+
+template <bool NT, typename V>
+__device__ __forceinline__ void store(V* p, const V& v) {
+  if (NT) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
+
 // 8 values of a float32 or bfloat16 array from value i0 on; those at or past n are 0
-template <bool B16>
+template <bool B16, bool NT = false>
 __device__ __forceinline__ void load_vals(const void* base, int64_t i0, int64_t n, bool whole, float* f) {
   if (whole) {
     if constexpr (B16) {
@@ -45,7 +59,7 @@ __device__ __forceinline__ void load_vals(const void* base, int64_t i0, int64_t 
         f[i] = (i & 1) ? __uint_as_float(q[i / 2] & 0xFFFF0000u) : __uint_as_float(q[i / 2] << 16);
     } else {
       const f32x4* p = (const f32x4*)((const float*)base + i0);
-      const f32x4 a = p[0], b = p[1];
+      const f32x4 a = load<NT>(p), b = load<NT>(p + 1);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         f[i] = a[i];
@@ -61,7 +75,7 @@ __device__ __forceinline__ void load_vals(const void* base, int64_t i0, int64_t 
   }
 }
 
-template <bool B16>
+template <bool B16, bool NT = false>
 __device__ __forceinline__ void store_vals(void* base, int64_t i0, int64_t n, bool whole, const float* f) {
   if (whole) {
     if constexpr (B16) {
@@ -71,8 +85,8 @@ __device__ __forceinline__ void store_vals(void* base, int64_t i0, int64_t n, bo
       *(u32x4*)((bf16_bits*)base + i0) = q;
     } else {
       f32x4* p = (f32x4*)((float*)base + i0);
-      p[0] = f32x4{f[0], f[1], f[2], f[3]};
-      p[1] = f32x4{f[4], f[5], f[6], f[7]};
+      store<NT>(p, f32x4{f[0], f[1], f[2], f[3]});
+      store<NT>(p + 1, f32x4{f[4], f[5], f[6], f[7]});
     }
     return;
   }
@@ -85,9 +99,10 @@ __device__ __forceinline__ void store_vals(void* base, int64_t i0, int64_t n, bo
 }
 
 // 8 bytes of codes from i0 on
+template <bool NT>
 __device__ __forceinline__ u32x2 load_codes(const void* base, int64_t i0, int64_t n, bool whole) {
   const uint8_t* p = (const uint8_t*)base + i0;
-  if (whole) return *(const u32x2*)p;
+  if (whole) return load<NT>((const u32x2*)p);
   u32x2 q = {0u, 0u};
 #pragma unroll
   for (int i = 0; i < kVals; ++i)
@@ -95,10 +110,11 @@ __device__ __forceinline__ u32x2 load_codes(const void* base, int64_t i0, int64_
   return q;
 }
 
+template <bool NT>
 __device__ __forceinline__ void store_codes(void* base, int64_t i0, int64_t n, bool whole, const u32x2& q) {
   uint8_t* p = (uint8_t*)base + i0;
   if (whole) {
-    *(u32x2*)p = q;
+    store<NT>((u32x2*)p, q);
     return;
   }
 #pragma unroll
@@ -164,18 +180,18 @@ struct Hyper {
 
 // WHOLE: the workgroup's chunk ends inside the tensor. All loads then go out together; with
 // the tail's branches between them the first was waited for before the second left.
-template <bool G16, bool P16, bool S8, bool WHOLE>
+template <bool G16, bool P16, bool S8, bool WHOLE, bool NT>
 __device__ __forceinline__ void update_chunk(const OptTensor& T, const Hyper& h, int64_t i0) {
   const int64_t n = T.n;
   const bool whole = WHOLE || i0 + kVals <= n;
   float g[kVals], p[kVals], mf[kVals], vf[kVals];
   double m[kVals], v[kVals];
   load_vals<G16>(T.grad, i0, n, whole, g);
-  load_vals<false>(P16 ? T.master : (const float*)T.param, i0, n, whole, p);
+  load_vals<false, NT>(P16 ? T.master : (const float*)T.param, i0, n, whole, p);
   const int64_t block = i0 / kQBlock;
   const bool inside = WHOLE || i0 < n;
   if constexpr (S8) {
-    const u32x2 mq = load_codes(T.m, i0, n, whole), vq = load_codes(T.v, i0, n, whole);
+    const u32x2 mq = load_codes<NT>(T.m, i0, n, whole), vq = load_codes<NT>(T.v, i0, n, whole);
     const double ms = pow2(inside ? (int)T.m_scale[block] - 127 : 0), vs = pow2(inside ? (int)T.v_scale[block] - 127 : 0);
     decode8<false>(mq, mf);
     decode8<true>(vq, vf);
@@ -185,8 +201,8 @@ __device__ __forceinline__ void update_chunk(const OptTensor& T, const Hyper& h,
       v[i] = (double)vf[i] * vs;
     }
   } else {
-    load_vals<false>(T.m, i0, n, whole, mf);
-    load_vals<false>(T.v, i0, n, whole, vf);
+    load_vals<false, NT>(T.m, i0, n, whole, mf);
+    load_vals<false, NT>(T.v, i0, n, whole, vf);
 #pragma unroll
     for (int i = 0; i < kVals; ++i) {
       m[i] = mf[i];
@@ -205,7 +221,7 @@ __device__ __forceinline__ void update_chunk(const OptTensor& T, const Hyper& h,
     const float move = h.step * mf[i] * __builtin_amdgcn_rcpf(fmaf(__builtin_amdgcn_sqrtf(vf[i]), h.root, h.eps));
     p[i] = p[i] - fmaf(h.decay, p[i], move);
   }
-  store_vals<false>(P16 ? (void*)T.master : T.param, i0, n, whole, p);
+  store_vals<false, NT>(P16 ? (void*)T.master : T.param, i0, n, whole, p);
   if constexpr (P16) store_vals<true>(T.param, i0, n, whole, p);
   if constexpr (S8) {
     double mt = 0.0, vt = 0.0;
@@ -226,23 +242,23 @@ __device__ __forceinline__ void update_chunk(const OptTensor& T, const Hyper& h,
       mq[i / 4] |= encode<false>(m[i], me, r & 0xFFFFu) << (8 * (i % 4));
       vq[i / 4] |= encode<true>(v[i], ve, r >> 16) << (8 * (i % 4));
     }
-    store_codes(T.m, i0, n, whole, mq);
-    store_codes(T.v, i0, n, whole, vq);
+    store_codes<NT>(T.m, i0, n, whole, mq);
+    store_codes<NT>(T.v, i0, n, whole, vq);
     if (inside && i0 % kQBlock == 0) {
       T.m_scale[block] = (uint8_t)(me + 127);
       T.v_scale[block] = (uint8_t)(ve + 127);
     }
   } else {
-    store_vals<false>(T.m, i0, n, whole, mf);
-    store_vals<false>(T.v, i0, n, whole, vf);
+    store_vals<false, NT>(T.m, i0, n, whole, mf);
+    store_vals<false, NT>(T.v, i0, n, whole, vf);
   }
 }
 
-template <bool G16, bool P16, bool S8>
+template <bool G16, bool P16, bool S8, bool NT>
 __device__ __forceinline__ void update(const OptTensor& T, const Hyper& h, int64_t first) {
   const int64_t i0 = first + threadIdx.x % kOptThreads * kVals;
-  if (first + kOptChunk <= T.n) update_chunk<G16, P16, S8, true>(T, h, i0);
-  else update_chunk<G16, P16, S8, false>(T, h, i0);
+  if (first + kOptChunk <= T.n) update_chunk<G16, P16, S8, true, NT>(T, h, i0);
+  else update_chunk<G16, P16, S8, false, NT>(T, h, i0);
 }
 
 // First chunks of a list's tensors, one or two a lane, loaded together; the tensor of chunk
@@ -287,6 +303,7 @@ __device__ __forceinline__ float clip_scale(double n, double max_norm) {
 // Four chunks a workgroup side by side: each workgroup takes part in the count at the end,
 // one after another (259 of them 2.7 us, 65 0.8).
 constexpr int kAdamSide = 4;
+template <bool NT>
 __global__ __launch_bounds__(kAdamSide * kOptThreads) void adamw_kernel(const OptList l, const OptHyper o,
                                                             int32_t* __restrict__ counter,
                                                             const float* __restrict__ lr_scale, const GradScale g) {
@@ -329,14 +346,14 @@ __global__ __launch_bounds__(kAdamSide * kOptThreads) void adamw_kernel(const Op
       h.key = mix32(o.seed + mix32(draw + (uint32_t)(l.base + j)));
       const int64_t i0 = (int64_t)(c - T.first) * kOptChunk;
       switch (T.flags) {  // the same for the chunk's waves
-        case 0: update<false, false, false>(T, h, i0); break;
-        case kGrad16: update<true, false, false>(T, h, i0); break;
-        case kParam16: update<false, true, false>(T, h, i0); break;
-        case kGrad16 | kParam16: update<true, true, false>(T, h, i0); break;
-        case kMoments8: update<false, false, true>(T, h, i0); break;
-        case kGrad16 | kMoments8: update<true, false, true>(T, h, i0); break;
-        case kParam16 | kMoments8: update<false, true, true>(T, h, i0); break;
-        default: update<true, true, true>(T, h, i0); break;
+        case 0: update<false, false, false, NT>(T, h, i0); break;
+        case kGrad16: update<true, false, false, NT>(T, h, i0); break;
+        case kParam16: update<false, true, false, NT>(T, h, i0); break;
+        case kGrad16 | kParam16: update<true, true, false, NT>(T, h, i0); break;
+        case kMoments8: update<false, false, true, NT>(T, h, i0); break;
+        case kGrad16 | kMoments8: update<true, false, true, NT>(T, h, i0); break;
+        case kParam16 | kMoments8: update<false, true, true, NT>(T, h, i0); break;
+        default: update<true, true, true, NT>(T, h, i0); break;
       }
     }
   }
@@ -419,7 +436,8 @@ hipError_t launch_adamw(const OptList& l, const OptHyper& h, int32_t* counter, c
                         const GradScale& gs, hipStream_t s) {
   // a workgroup's 16 waves of up to 128 registers fill a CU
   const unsigned grid = (unsigned)max(1, min((l.chunks + kAdamSide - 1) / kAdamSide, device_cus()));
-  hipLaunchKernelGGL(adamw_kernel, dim3(grid), dim3(kAdamSide * kOptThreads), 0, s, l, h, counter, lr_scale, gs);
+  constexpr int kLong = (8 << 20) / kOptChunk;  // 8 million values
+  hipLaunchKernelGGL(l.chunks >= kLong ? adamw_kernel<true> : adamw_kernel<false>, dim3(grid), dim3(kAdamSide * kOptThreads), 0, s, l, h, counter, lr_scale, gs);
   return hipGetLastError();
 }
 
