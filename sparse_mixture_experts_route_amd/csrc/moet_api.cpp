@@ -274,6 +274,12 @@ moe_status_t check_step(const moet_tensor_t* tensors, int32_t count, const moet_
 moe_status_t run_step(const moet_tensor_t* tensors, int32_t count, const moet_adamw_t* opt, int32_t* counter,
                       const float* lr_scale, const GradScale& gs, hipStream_t s) {
   const OptHyper h = {opt->lr, opt->beta1, opt->beta2, std::log(opt->beta1), std::log(opt->beta2), (float)opt->eps, opt->seed};
+  int64_t values = 0, grads = 0;
+  for (int j = 0; j < count; ++j) {
+    values += tensors[j].n;
+    grads += tensors[j].n * (int64_t)elem_size(tensors[j].grad_dtype);
+  }
+  const bool past_caches = values >= (int64_t)8 << 20 && grads <= (int64_t)192 << 20;  // see optim.hip
   OptList l;
   int i = 0;
   do {
@@ -290,7 +296,7 @@ moe_status_t run_step(const moet_tensor_t* tensors, int32_t count, const moet_ad
       l.chunks += (int32_t)((t.n + kOptChunk - 1) / kOptChunk);
     }
     l.last = i >= count;
-    if (launch_adamw(l, h, counter, lr_scale, gs, s) != hipSuccess) return MOE_ERR_HIP;
+    if (launch_adamw(l, h, counter, lr_scale, gs, past_caches, s) != hipSuccess) return MOE_ERR_HIP;
   } while (i < count);
   return MOE_OK;
 }

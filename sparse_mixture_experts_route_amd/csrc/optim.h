@@ -67,8 +67,9 @@ struct GradScale {
 
 static_assert(sizeof(OptList) + sizeof(OptHyper) + sizeof(GradScale) + 16 <= 4096 && sizeof(NormList) + 64 <= 4096, "kernel arguments");
 
+// past_caches: for master copies and moments
 hipError_t launch_adamw(const OptList& l, const OptHyper& h, int32_t* counter, const float* lr_scale,
-                        const GradScale& gs, hipStream_t s);
+                        const GradScale& gs, bool past_caches, hipStream_t s);
 // One launch over a list; the partial sums in `slots` [kNormSlots]
 hipError_t launch_square_sums(const NormList& l, double* slots, hipStream_t s);
 hipError_t launch_norm_scale(const double* slots, double max_norm, float* norm, float* scale, hipStream_t s);

@@ -34,9 +34,11 @@ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
   return x ^ (x >> 16);
 }
 
-// NT: a long list's master copies and moments pass by the caches, which would not keep
-// them until the next step (67 million values, 32-bit moments with the norm 408 -> 385 us, 8-bit
-// 256 -> 234; 3.6 million in 48 tensors, the same ones again, 24.7 -> 26.0)
+// NT: master copies and moments pass by the last-level cache (256 MB), so that the
+// gradients that the norm has just read stay there: a list of 8 million values or more
+// whose gradients are at most 192 MB. Step with norm, NT / through the caches, 32-bit
+// moments and 8-bit ones: 4 M values (through) 34 and 26 us, 8 M 54 / 58 and 39 / 43, 67 M
+// 404 / 409 and 247 / 259, 134 M 850 / 817 and 511 / 512, 268 M 1720 / 1631 and 1031 / 1031.
 template <bool NT, typename V>
 __device__ __forceinline__ V load(const V* p) {
   return NT ? __builtin_nontemporal_load(p) : *p;
@@ -433,11 +435,10 @@ __global__ __launch_bounds__(kNormSlots) void norm_scale_kernel(const double* __
 }  // namespace
 
 hipError_t launch_adamw(const OptList& l, const OptHyper& h, int32_t* counter, const float* lr_scale,
-                        const GradScale& gs, hipStream_t s) {
+                        const GradScale& gs, bool past_caches, hipStream_t s) {
   // a workgroup's 16 waves of up to 128 registers fill a CU
   const unsigned grid = (unsigned)max(1, min((l.chunks + kAdamSide - 1) / kAdamSide, device_cus()));
-  constexpr int kLong = (8 << 20) / kOptChunk;  // 8 million values
-  hipLaunchKernelGGL(l.chunks >= kLong ? adamw_kernel<true> : adamw_kernel<false>, dim3(grid), dim3(kAdamSide * kOptThreads), 0, s, l, h, counter, lr_scale, gs);
+  hipLaunchKernelGGL(past_caches ? adamw_kernel<true> : adamw_kernel<false>, dim3(grid), dim3(kAdamSide * kOptThreads), 0, s, l, h, counter, lr_scale, gs);
   return hipGetLastError();
 }
 

@@ -189,3 +189,33 @@ def test_block_of_odd_sizes(moe, T, E, K):
     # gradient of the second bias is the sum of dy, of bfloat16 values in float32 and rounded once
     s = f64(dy).sum(0)
     assert_within("c2", f64(block.grads["c2"]), s, (T + 40) * U32 * np.abs(f64(dy)).sum(0) + 2.0 ** -8 * np.abs(s))
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("pt,gt", [(BF, BF), (BF, F32), (F32, BF), (F32, F32)])
+def test_long_lists_take_the_same_step(moe, bits, pt, gt):
+    """Lists of 8 million values and more (loads and stores past the caches): the bits of a short list's step, whose
+    tensor is the beginning of theirs."""
+    announce(f"adamw long list bits={bits} {pt} {gt}")
+    n, m = (8 << 20) + 1237, 1 << 20
+    g = gen(16)
+    p = (torch.randn(n, generator=g, device="cuda") * 0.1).to(pt)
+    gr = torch.randn(n, generator=g, device="cuda").to(gt)
+    q, gq = p[:m].clone(), gr[:m].clone()
+    a, b = (moe.AdamW([t], lr=LR, bits=[bits], seed=4) for t in (p, q))
+    for _ in range(2):
+        a.step([gr])
+        b.step([gq])
+    torch.cuda.synchronize()
+    assert torch.equal(p[:m], q) and torch.equal(a.counter, b.counter)
+    for x, y in ((a.m[0][:m], b.m[0]), (a.v[0][:m], b.v[0])):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    assert torch.isfinite(p.float()).all() and bool((a.v[0][-2000:].float() > 0).all())
+    # the tail, past the last whole chunk: as a tensor of its own, whose moments in 32 bits do not depend on its place
+    if bits == 32:
+        t = (n // 2048) * 2048
+        c = moe.AdamW([torch.zeros(n - t, device="cuda")], lr=LR, bits=[32])
+        for _ in range(2):
+            c.step([gr[t:].clone()])
+        torch.cuda.synchronize()
+        assert torch.equal(a.m[0][t:], c.m[0]) and torch.equal(a.v[0][t:], c.v[0])
