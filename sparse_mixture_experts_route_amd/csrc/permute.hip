@@ -39,11 +39,19 @@ constexpr int kTB = kPermuteTokensPerBlock;  // tokens per block, one thread eac
 constexpr int kWords = kTB / 32;             // mask words per expert
 constexpr int kPitch = kWords + 1;           // of them in LDS: lanes with different experts take different banks
 
+// Selections j0 .. j0 + 7 of token t, loaded together (-1 past k and past the tokens)
+__device__ __forceinline__ void load_named(const int32_t* __restrict__ idx, int64_t T, int k, int64_t t, int j0, int* ev) {
+#pragma unroll
+  for (int u = 0; u < 8; ++u) ev[u] = t < T && j0 + u < k ? idx[t * k + j0 + u] : -1;
+}
+
+// `first`: this thread's token's first eight selections.
 // REPEATS: a token may name an expert twice. `extra[e]` then counts the selections
 // that a mask has no bit for, and the result says whether the block has any.
 template <bool REPEATS = false>
 __device__ __forceinline__ bool build_mask(const int32_t* __restrict__ idx, int64_t T, int k, int E,
-                                           uint32_t (*mask)[kPitch], int64_t t0, int* extra = nullptr) {
+                                           uint32_t (*mask)[kPitch], int64_t t0, const int* first,
+                                           int* extra = nullptr) {
   uint32_t* flat = &mask[0][0];
   for (int i = threadIdx.x; i < E * kPitch; i += kTB) flat[i] = 0u;
   if (REPEATS && (int)threadIdx.x < E) extra[threadIdx.x] = 0;
@@ -52,13 +60,12 @@ __device__ __forceinline__ bool build_mask(const int32_t* __restrict__ idx, int6
   bool again = false;
   if (t < T) {
     const uint32_t bit = 1u << (threadIdx.x & 31);
-    for (int j0 = 0; j0 < k; j0 += 8) {  // eight loads in flight
+    for (int j0 = 0; j0 < k; j0 += 8) {
       int ev[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) ev[u] = j0 + u < k ? idx[t * k + j0 + u] : -1;
+      if (j0) load_named(idx, T, k, t, j0, ev);
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const int e = ev[u];
+        const int e = j0 ? ev[u] : first[u];
         if ((unsigned)e >= (unsigned)E) continue;
         if (!REPEATS) {
           atomicOr(&mask[e][threadIdx.x >> 5], bit);
@@ -82,7 +89,9 @@ __global__ __launch_bounds__(kTB) void hist_kernel(const int32_t* __restrict__ i
   __shared__ int extra[REPEATS ? 256 : 1];
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < nzero; i += kTB) zero[i] = 0;
-  build_mask<REPEATS>(idx, T, k, E, mask, (int64_t)blockIdx.x * kTB, extra);
+  int first[8];
+  load_named(idx, T, k, (int64_t)blockIdx.x * kTB + threadIdx.x, 0, first);
+  build_mask<REPEATS>(idx, T, k, E, mask, (int64_t)blockIdx.x * kTB, first, extra);
   const int e = threadIdx.x;
   if (e < E) {
     int c = REPEATS ? extra[e] : 0;
@@ -247,18 +256,32 @@ __global__ __launch_bounds__(kTB) void scatter_kernel(const int32_t* __restrict_
   __shared__ int extra[REPEATS ? 256 : 1];
   const int64_t t0 = (int64_t)blockIdx.x * kTB;
   const int e0 = threadIdx.x;  // kTB = 256 threads: one expert slot each
+  int first[8];  // on their way while the counts are added
+  load_named(idx, T, k, t0 + threadIdx.x, 0, first);
   if constexpr (SCAN) {
+    // the blocks' counts of an expert by as many threads as there are for each
+    __shared__ int32_t s_tot[kTB], s_prev[kTB];
+    const int side = E <= 32 ? 8 : E <= 64 ? 4 : E <= 128 ? 2 : 1, ep = kTB / side, ec = threadIdx.x % ep;
     int32_t tot = 0, before = 0;
-    if (e0 < E)
-      for (int64_t b0 = 0; b0 < nb; b0 += 16) {  // sixteen loads in flight
+    if (ec < E)
+      for (int64_t b0 = threadIdx.x / ep; b0 < nb; b0 += 16 * side) {  // sixteen loads in flight
         int32_t c[16];
 #pragma unroll
-        for (int u = 0; u < 16; ++u) c[u] = b0 + u < nb ? blockcounts[(b0 + u) * E + e0] : 0;
+        for (int u = 0; u < 16; ++u) c[u] = b0 + u * side < nb ? blockcounts[(b0 + u * side) * E + ec] : 0;
 #pragma unroll
         for (int u = 0; u < 16; ++u) {
           tot += c[u];
-          before += b0 + u < (int64_t)blockIdx.x ? c[u] : 0;
+          before += b0 + u * side < (int64_t)blockIdx.x ? c[u] : 0;
         }
+      }
+    s_tot[threadIdx.x] = tot;
+    s_prev[threadIdx.x] = before;
+    __syncthreads();
+    tot = before = 0;
+    if (e0 < E)
+      for (int i = 0; i < side; ++i) {
+        tot += s_tot[i * ep + e0];
+        before += s_prev[i * ep + e0];
       }
     // inclusive scan of the totals over the 256 expert slots: within waves, then over the four
     int incl = tot;
@@ -281,7 +304,7 @@ __global__ __launch_bounds__(kTB) void scatter_kernel(const int32_t* __restrict_
     if (e0 < E) s_base[e0] = blockcounts[(int64_t)blockIdx.x * E + e0];
   }
   // this block's first row per expert is visible after build_mask's barriers
-  const bool repeated = build_mask<REPEATS>(idx, T, k, E, mask, t0, extra);
+  const bool repeated = build_mask<REPEATS>(idx, T, k, E, mask, t0, first, extra);
   const int64_t t = t0 + threadIdx.x;
   if (REPEATS && repeated) {
     scatter_repeats(idx, T, k, E, t, mask, s_base, perm, inv);
@@ -303,12 +326,11 @@ __global__ __launch_bounds__(kTB) void scatter_kernel(const int32_t* __restrict_
   // the selections in groups of 8, whose indices are loaded together
   for (int j0 = 0; j0 < k; j0 += 8) {
     int ev[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) ev[u] = j0 + u < k ? idx[t * k + j0 + u] : -1;
+    if (j0) load_named(idx, T, k, t, j0, ev);
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       if (j0 + u < k) {
-        const int e = ev[u];
+        const int e = j0 ? ev[u] : first[u];
         int32_t r = -1;
         if ((unsigned)e < (unsigned)E) {
           r = s_base[e] + s_before[e][w] + __popc(mask[e][w] & below);

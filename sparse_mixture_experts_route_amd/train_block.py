@@ -33,7 +33,7 @@ class MoETrainBlock:
     by the caller. The buffers' memory is not handed out again while work of a torch
     stream is in flight on it; for a raw stream handle the caller keeps the object until
     that work has ended. x, residual and dy are kept by the caller until the backward
-    pass has been enqueued.
+    pass has ended; it may be called again, with another dy, before the next step.
     """
 
     def __init__(self, T: int, d_model: int, E: int, k: int, d_expert: int, params: Dict[str, torch.Tensor],
