@@ -168,9 +168,11 @@ moe_status_t moet_adamw(const moet_tensor_t* tensors, int32_t count, const moet_
 
 /* Norm of all gradients of a list as one vector, and the factor that clips it:
  *   norm  [1] float32 = sqrt(sum of squares), added in 64 bits in a fixed order
- *   scale [1] float32 = min(1, max_norm / norm), NaN when the norm is not finite
+ *   scale [1] float32 = min(1, max_norm / norm), NaN when a gradient is not finite
  *         (moet_adamw then leaves the step out); may be NULL
- * grad, grad_dtype and n of the tensors are used. max_norm > 0.
+ * The factor is taken from the norm in 64 bits: a norm past float32 is written as
+ * infinity and still has its factor. grad, grad_dtype and n of the tensors are used.
+ * max_norm > 0, infinity included: norm and guard without clipping.
  *   ws  MOET_GRAD_NORM_WS_BYTES */
 moe_status_t moet_grad_norm(const moet_tensor_t* tensors, int32_t count, double max_norm, float* norm, float* scale,
                             void* ws, size_t ws_bytes, void* stream);

@@ -297,9 +297,10 @@ __device__ __forceinline__ double block_sum(double v, double* slots) {
   return v;
 }
 
-// The factor that clips gradients of norm n, NaN when it is not finite
+// The factor that clips gradients of norm n, NaN when it is not finite (an infinite
+// max_norm is not below an infinite n)
 __device__ __forceinline__ float clip_scale(double n, double max_norm) {
-  return n <= max_norm ? 1.0f : n < INFINITY ? (float)(max_norm / n) : NAN;
+  return !(n < INFINITY) ? NAN : n <= max_norm ? 1.0f : (float)(max_norm / n);
 }
 
 // Four chunks a workgroup side by side: each workgroup takes part in the count at the end,

@@ -20,7 +20,7 @@ class AdamW:
     values (tensors of fewer than `least` values keep 32 bits; bits may also be one
     number per parameter). lr_factor and weight_decay may be numbers or one per
     parameter. With max_norm the gradients are clipped to that norm, and a step
-    whose gradients are not finite is left out altogether.
+    whose gradients are not finite is left out altogether (max_norm=inf: that alone).
 
     A step only enqueues work: it can be captured into a graph. It reads lr when it
     is enqueued, and at every replay `lr_scale`, a float32 tensor of this object
