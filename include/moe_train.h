@@ -127,8 +127,8 @@ moe_status_t moet_linear_backward(const moe_problem_t* p, const void* x, const v
  * since an update divides by its root. Element i of tensor j at step t draws, in 32-bit arithmetic,
  *   mix((lo32(i) + mix(seed + mix(0x9E3779B9 t + j))) ^ (0x9E3779B9 hi32(i)))
  *   mix(x): x ^= x >> 16; x *= 0x7FEB352D; x ^= x >> 15; x *= 0x846CA68B; x ^= x >> 16
- * whose low half is m's number and whose high half v's. What is not finite
- * becomes a NaN code. */
+ * whose low half is m's number and whose high half v's. What is not finite, or above
+ * top 2^120, becomes a NaN code. */
 typedef struct {
   void* param;        /* [n] of param_dtype, updated */
   const void* grad;   /* [n] of grad_dtype */
@@ -155,7 +155,8 @@ typedef struct {
 /* One AdamW step, with t = counter[0] + 1 and g = grad grad_scale:
  *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
  *   param -= lr lr_scale lr_factor (m / (1 - beta1^t) / (sqrt(v / (1 - beta2^t)) + eps) + weight_decay param)
- * from the moments before they are rounded, which are taken in 64 bits.
+ * from the moments before they are rounded, which are taken in 64 bits; the move is made
+ * from their float32 values, so one whose v is past float32 moves by its decay alone.
  *   tensors  HOST array of count <= MOET_MAX_TENSORS entries, read during the call only
  *   opt      HOST pointer: finite lr >= 0, beta1 and beta2 in [0, 1), 1e-15 <= eps <= 1e15
  *   counter  [2] int32: steps taken, and 0, which the call uses. It is advanced by one

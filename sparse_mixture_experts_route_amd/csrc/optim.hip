@@ -147,6 +147,23 @@ __device__ __forceinline__ float up32(double x) {
   return (double)f < x && f < INFINITY ? __uint_as_float(__float_as_uint(f) + 1u) : f;
 }
 
+// Exponent of the scale of a block whose largest second moment is x >= 0: the smallest e
+// with x <= 1.75 2^(15 + e), in [-120, 120]. From the upper half of the double, a unit up
+// where the lower one is not 0: float32 ends at 2^128, the codes 2^8 further on.
+__device__ __forceinline__ int scale_exp_v(double x) {
+  uint32_t hi = (uint32_t)__double2hiint(x) + (__double2loint(x) != 0 ? 1u : 0u);
+  auto turn = [&](auto ctrl) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)hi, decltype(ctrl)::value, 0xF, 0xF, true);
+  };
+  // over the lanes of a DPP row, which have the 128 values of a scale
+  hi = max(hi, turn(IntC<0x128>{}));
+  hi = max(hi, turn(IntC<0x124>{}));
+  hi = max(hi, turn(IntC<0x122>{}));
+  hi = max(hi, turn(IntC<0x121>{}));
+  // what is above 1.75 carries into the exponent's field
+  return min(max((int)((hi + 0x3FFFFu) >> 20) - (1023 + 15), -120), 120);
+}
+
 // Code of x / 2^e with random number r < 2^16: e4m3 (3 bits of mantissa, bias 7) or
 // e5m2 (2 bits, bias 15). x is sig 2^(exp - 20) with 21 bits of sig from the double's
 // upper half; shifted to units of 2^-16 spacings, below the smallest normal those of
@@ -228,14 +245,12 @@ __device__ __forceinline__ void update_chunk(const OptTensor& T, const Hyper& h,
   if constexpr (S8) {
     double mt = 0.0, vt = 0.0;
 #pragma unroll
-    for (int i = 0; i < kVals; ++i) {  // values past the end are 0
+    for (int i = 0; i < kVals; ++i) {  // values past the end are 0; NaN is left out
       mt = fmax(mt, fabs(m[i]));
       vt = fmax(vt, v[i]);
     }
-    // the lanes of a DPP row have the 128 values of a scale; 57344 is 1.75 2^15, 448 is 1.75 2^8
-    const int me = scale_byte(row16_max(up32(mt))) - 127;
-    const uint32_t vu = __float_as_uint(row16_max(up32(vt)));
-    const int ve = min(max((int)((vu + 0x1FFFFFu) >> 23) - 142, -120), 120);
+    // (a first moment past float32 has the largest scale: 448 2^119 is within it)
+    const int me = scale_byte(row16_max(up32(mt))) - 127, ve = scale_exp_v(vt);
     u32x2 mq = {0u, 0u}, vq = {0u, 0u};
     const uint32_t high = (uint32_t)((uint64_t)i0 >> 32) * 0x9E3779B9u;  // a chunk does not cross 2^32
 #pragma unroll

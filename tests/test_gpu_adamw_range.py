@@ -1,0 +1,49 @@
+"""Moments at the ends of their types' ranges, against float64."""
+
+import numpy as np
+import pytest
+import torch
+
+from ext_helpers import gen
+from gpu_helpers import announce, f64, needs_gpu
+from oracle import train_ops as to
+from test_gpu_adamw import B1, B2, BF, EPS, F32, LR
+
+pytestmark = [pytest.mark.gpu, needs_gpu]
+
+# Largest second moment of each block of 128. Float32 ends at 3.4e38; the codes, 57344 2^120, at 7.62e40.
+TOPS = [1e36, 3.3e38, 3.5e38, 5.9e38, 6.0e38, 1e39, 3.3e39, 1e40, 4.1e40, 7.5e40, 8e40, 1e42]
+
+
+def codes(t):
+    return t.view(torch.uint8).cpu().numpy()
+
+
+@pytest.mark.parametrize("gt", [F32, BF])
+def test_second_moments_past_float32(moe, gt):
+    announce(f"adamw second moments past float32 {gt}")
+    n = 128 * len(TOPS)
+    spread = torch.exp2(-12 * torch.rand((len(TOPS), 128), generator=gen(31), device="cuda"))
+    spread[:, 17] = 1.0
+    g = (spread * torch.tensor([(v / (1 - B2)) ** 0.5 for v in TOPS], device="cuda")[:, None]).reshape(-1).to(gt)
+    p = torch.full((n,), 2.0, device="cuda")
+    opt = moe.AdamW([p], lr=LR, betas=(B1, B2), eps=EPS, weight_decay=0.0, bits=[8], seed=5)
+    opt.step([g])
+    torch.cuda.synchronize()
+    x = f64(g)
+    m, v = (1 - B1) * x, ((1 - B2) * x) * x
+    r = to.draws(n, 5, 1, 0)
+    for name, val, rr, c, s, tab in (("m", m, r & 0xFFFF, opt.m[0], opt.m_scale[0], to.E4M3_POS),
+                                     ("v", v, r >> 16, opt.v[0], opt.v_scale[0], to.E5M2_POS)):
+        want, e = to.round_stochastic(val, rr, tab, name == "v")
+        assert np.array_equal(s.cpu().numpy().astype(np.int64) - 127, e), name
+        assert np.array_equal(codes(c), want), name
+    held = v <= 57344 * 2.0 ** 120
+    assert held[:128 * 10].all() and not held[-128 * 2:].all()
+    assert np.array_equal(codes(opt.v[0]) != 0x7F, held)
+    # the move is made in float32, which does not hold the larger ones: such a value moves by nothing
+    far = torch.from_numpy(v > 3.5e38).cuda()
+    assert bool((p[far] == 2.0).all()) and torch.isfinite(p).all()
+    opt.step([torch.zeros_like(g)])
+    torch.cuda.synchronize()
+    assert torch.equal(torch.isfinite(p), torch.from_numpy(held).cuda())
