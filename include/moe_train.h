@@ -128,7 +128,7 @@ moe_status_t moet_linear_backward(const moe_problem_t* p, const void* x, const v
  *   mix((lo32(i) + mix(seed + mix(0x9E3779B9 t + j))) ^ (0x9E3779B9 hi32(i)))
  *   mix(x): x ^= x >> 16; x *= 0x7FEB352D; x ^= x >> 15; x *= 0x846CA68B; x ^= x >> 16
  * whose low half is m's number and whose high half v's. What is not finite, or above
- * top 2^120, becomes a NaN code. */
+ * top 2^120, becomes a NaN code; max is that of the values that are not NaN. */
 typedef struct {
   void* param;        /* [n] of param_dtype, updated */
   const void* grad;   /* [n] of grad_dtype */

@@ -136,7 +136,7 @@ def round_stochastic(x: np.ndarray, r: np.ndarray, table: np.ndarray, keep: bool
     n = x.size
     pad = -n % 128
     a = np.abs(np.pad(x, (0, pad))).reshape(-1, 128)
-    e = block_exponent(np.max(np.where(np.isfinite(a), a, np.inf), axis=1), table[-1])
+    e = block_exponent(np.max(np.where(np.isnan(a), 0.0, a), axis=1), table[-1])  # NaN is left out
     v = np.ldexp(a, -e[:, None].astype(np.int32)).reshape(-1)[:n]
     bad = ~(v <= table[-1])
     v = np.where(bad, 0.0, v)

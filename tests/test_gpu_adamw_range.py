@@ -47,3 +47,26 @@ def test_second_moments_past_float32(moe, gt):
     opt.step([torch.zeros_like(g)])
     torch.cuda.synchronize()
     assert torch.equal(torch.isfinite(p), torch.from_numpy(held).cuda())
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_blocks_with_what_is_not_finite(moe, bad):
+    """A NaN is left out of its block's scale, an infinity gives its block the largest one; each becomes a NaN code."""
+    announce(f"adamw scale of a block with {bad}")
+    n = 384
+    g = torch.randn(n, generator=gen(32), device="cuda")
+    g[5], g[130] = bad, bad
+    p = torch.zeros(n, device="cuda")
+    opt = moe.AdamW([p], lr=LR, betas=(B1, B2), eps=EPS, weight_decay=0.0, bits=[8], seed=6)
+    opt.step([g])
+    torch.cuda.synchronize()
+    x = f64(g)
+    r = to.draws(n, 6, 1, 0)
+    lost = ~np.isfinite(x)
+    for name, val, rr, c, s, tab in (("m", (1 - B1) * x, r & 0xFFFF, opt.m[0], opt.m_scale[0], to.E4M3_POS),
+                                     ("v", ((1 - B2) * x) * x, r >> 16, opt.v[0], opt.v_scale[0], to.E5M2_POS)):
+        want, e = to.round_stochastic(val, rr, tab, name == "v")
+        assert np.array_equal(s.cpu().numpy().astype(np.int64) - 127, e), name
+        assert np.isnan(bad) or e.tolist() == [120, 120, e[2]]
+        assert np.array_equal(codes(c)[~lost], want[~lost]) and (codes(c)[lost] & 0x7F == 0x7F).all(), name
+    assert np.array_equal(np.isfinite(f64(p)), ~lost)
