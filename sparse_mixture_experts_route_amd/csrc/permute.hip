@@ -195,49 +195,82 @@ __global__ __launch_bounds__(kScanThreads) void scan_kernel(const int32_t* __res
 // separate scan launch is skipped.
 constexpr int kFusedScanBlocks = 64;
 
-// Rows of a block in which a token names an expert more than once. Level m has the bits
-// of the tokens that name an expert m times or more: a selection's rank is the sum over the
-// levels of the bits below its token, and the token's own earlier ones.
-// (Ranks are added up in inv; a token's entries are its own thread's.)
+// Rows of a block in which a token names an expert more than once, for 32 experts at a
+// time: how often each token names each, the sums over the tokens before, and the rows
+// in the order of a token's selections. Each selection is read twice for every 32
+// experts, however often an expert is named. (A token's entries are its own thread's.
+// The sums stay below 2^16: 256 tokens of at most 256 selections.)
+// Ranks by levels of repetition, each counting a token's earlier selections anew, read some
+// k^3 / 2 selections a thread where a token has them all of one expert. Dispatch of 64-wide
+// rows, experts drawn at random, us in a graph, levels / now: 8192 tokens of 8 among 64
+// experts 62 / 26, among 256 54 / 53, 4096 of 8 among 8 80 / 20, of 40 among 64 1130 / 75;
+// 512 tokens of 256 selections of one expert 844.
+constexpr int kRepeatExperts = 32;
+constexpr int kRepeatPitch = kTB + 8;  // whole 16-byte pieces, different experts' in different banks
+
 __device__ __noinline__ void scatter_repeats(const int32_t* __restrict__ idx, int64_t T, int k, int E, int64_t t,
-                                             uint32_t (*mask)[kPitch], const int32_t* s_base,
-                                             int32_t* __restrict__ perm, int32_t* inv) {
-  const int w = threadIdx.x >> 5;
-  const uint32_t bit = 1u << (threadIdx.x & 31);
-  auto named = [&](int j) { return t < T ? idx[t * k + j] : -1; };
-  auto before = [&](int j, int e) {  // the token's selections of e ahead of j
-    int n = 0;
-    for (int i = 0; i < j; ++i) n += idx[t * k + i] == e;
-    return n;
-  };
-  for (int m = 0;; ++m) {
+                                             uint16_t (*named)[kRepeatPitch], const int32_t* s_base,
+                                             int32_t* __restrict__ perm, int32_t* __restrict__ inv) {
+  constexpr int PARTS = kTB / kRepeatExperts, LEN = kTB / PARTS;  // threads of an expert, tokens of each
+  const int me = threadIdx.x, own = me / PARTS, part = me % PARTS;
+  for (int e0 = 0; e0 < E; e0 += kRepeatExperts) {
+    __syncthreads();  // the counts' last readers are through
+    for (int i = me; i < kRepeatExperts * kRepeatPitch / 8; i += kTB) ((u32x4*)named)[i] = u32x4{0u, 0u, 0u, 0u};
     __syncthreads();
-    uint32_t* flat = &mask[0][0];
-    for (int i = threadIdx.x; i < E * kPitch; i += kTB) flat[i] = 0u;
-    __syncthreads();
-    bool more = false;
-    for (int j = 0; j < k; ++j) {
-      const int e = named(j);
-      if ((unsigned)e >= (unsigned)E) continue;
-      const int n = before(j, e);
-      if (n == m) atomicOr(&mask[e][w], bit);
-      more |= n > m;
-    }
-    more = __syncthreads_or(more);
-    for (int j = 0; j < k; ++j) {
-      const int e = named(j);
-      if (t >= T) break;
-      int r = -1;
-      if ((unsigned)e < (unsigned)E) {
-        r = m == 0 ? s_base[e] + before(j, e) : inv[t * k + j];
-        r += __popc(mask[e][w] & (bit - 1u));
-        for (int i = 0; i < w; ++i) r += __popc(mask[e][i]);
-        if (!more) perm[r] = (int32_t)t;
+    for (int j0 = 0; j0 < k; j0 += 8) {
+      int ev[8];
+      load_named(idx, T, k, t, j0, ev);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const unsigned e = (unsigned)ev[u] - (unsigned)e0;
+        if (ev[u] < E && e < (unsigned)kRepeatExperts) ++named[e][me];
       }
-      inv[t * k + j] = r;
     }
-    if (!more) return;
+    __syncthreads();
+    u32x4* const mine = (u32x4*)&named[own][part * LEN];
+    u32x4 n[LEN / 8];
+    uint32_t sum = 0;
+#pragma unroll
+    for (int i = 0; i < LEN / 8; ++i) {
+      n[i] = mine[i];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) sum += (n[i][w] & 0xFFFFu) + (n[i][w] >> 16);
+    }
+    uint32_t before = sum;
+#pragma unroll
+    for (int o = 1; o < PARTS; o <<= 1) {
+      const uint32_t v = __shfl_up(before, o, PARTS);
+      if (part >= o) before += v;
+    }
+    before -= sum;
+#pragma unroll
+    for (int i = 0; i < LEN / 8; ++i) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t lo = n[i][w] & 0xFFFFu, hi = n[i][w] >> 16;
+        n[i][w] = before | ((before + lo) << 16);
+        before += lo + hi;
+      }
+      mine[i] = n[i];
+    }
+    __syncthreads();
+    for (int j0 = 0; j0 < k; j0 += 8) {
+      int ev[8];
+      load_named(idx, T, k, t, j0, ev);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const unsigned e = (unsigned)ev[u] - (unsigned)e0;
+        if (ev[u] < E && e < (unsigned)kRepeatExperts) {
+          const int r = s_base[ev[u]] + named[e][me]++;
+          perm[r] = (int32_t)t;
+          inv[t * k + j0 + u] = r;
+        }
+      }
+    }
   }
+  if (t >= T) return;
+  for (int j = 0; j < k; ++j)
+    if ((unsigned)idx[t * k + j] >= (unsigned)E) inv[t * k + j] = -1;
 }
 
 // SCAN: `blockcounts` holds the per-block counts of hist_kernel (nb blocks);
@@ -250,9 +283,12 @@ __global__ __launch_bounds__(kTB) void scatter_kernel(const int32_t* __restrict_
                                                       const int32_t* __restrict__ blockcounts, int64_t nb,
                                                       int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
                                                       int32_t* __restrict__ perm, int32_t* __restrict__ inv) {
-  __shared__ uint32_t mask[256][kPitch];
+  // masks and the counts of the words before, or scatter_repeats' counts
+  __shared__ __attribute__((aligned(16))) uint32_t s_words[2][256][kPitch];
+  uint32_t(*const mask)[kPitch] = s_words[0];
+  int32_t(*const s_before)[kPitch] = (int32_t(*)[kPitch])s_words[1];
+  static_assert(sizeof(uint16_t) * kRepeatExperts * kRepeatPitch <= sizeof(s_words), "scatter_repeats' counts");
   __shared__ int32_t s_base[256];
-  __shared__ int32_t s_before[256][kPitch];
   __shared__ int extra[REPEATS ? 256 : 1];
   const int64_t t0 = (int64_t)blockIdx.x * kTB;
   const int e0 = threadIdx.x;  // kTB = 256 threads: one expert slot each
@@ -307,7 +343,7 @@ __global__ __launch_bounds__(kTB) void scatter_kernel(const int32_t* __restrict_
   const bool repeated = build_mask<REPEATS>(idx, T, k, E, mask, t0, first, extra);
   const int64_t t = t0 + threadIdx.x;
   if (REPEATS && repeated) {
-    scatter_repeats(idx, T, k, E, t, mask, s_base, perm, inv);
+    scatter_repeats(idx, T, k, E, t, (uint16_t(*)[kRepeatPitch])s_words, s_base, perm, inv);
     return;
   }
   // tokens of each expert in the words before each
