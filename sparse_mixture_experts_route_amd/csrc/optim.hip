@@ -341,7 +341,9 @@ __global__ __launch_bounds__(kAdamSide * kOptThreads) void adamw_kernel(const Op
   }
   const bool skip = gs != gs;
   if (!skip) {
-    // 1 - b^t; with b below 1 - 1e-8 the difference is good for float32
+    // 1 - b^t, good for float32 for every b below 1: 1 - b is a multiple of 2^-53 and so is, to first
+    // order, 1 - b^t, which the difference of a rounded b^t therefore has exactly; the second order
+    // is off by half of t (1 - b) of it where it is lost, below 2^-27 (5.3e-9 the most of 2^24 pairs)
     const double t = (double)(before + 1);
     const float c1 = (float)(1.0 - exp(t * o.log_beta1)), c2 = (float)(1.0 - exp(t * o.log_beta2));
     const float lr = (float)(o.lr * (double)ls);
@@ -376,8 +378,8 @@ __global__ __launch_bounds__(kAdamSide * kOptThreads) void adamw_kernel(const Op
     }
   }
   if (!l.last) return;
-  // The last workgroup to come here advances the counter: all have read it by then,
-  // this one's other waves included (the barrier waits for their loads). Nothing else
+  // The last workgroup to come here advances the counter: by then a wave that had a chunk has
+  // made its updates from `before`, and one that had none does not need it. Nothing else
   // is passed on, so no fence: one of the device's scope writes the L2 back.
   __syncthreads();
   if (threadIdx.x == 0) {

@@ -1,11 +1,11 @@
-"""Moments at the ends of their types' ranges, against float64."""
+"""Moments at the ends of their types' ranges, and factors beta next to 1, against float64."""
 
 import numpy as np
 import pytest
 import torch
 
-from ext_helpers import gen
-from gpu_helpers import announce, f64, needs_gpu
+from ext_helpers import assert_within, gen
+from gpu_helpers import U32, announce, f64, needs_gpu
 from oracle import train_ops as to
 from test_gpu_adamw import B1, B2, BF, EPS, F32, LR
 
@@ -70,3 +70,27 @@ def test_blocks_with_what_is_not_finite(moe, bad):
         assert np.isnan(bad) or e.tolist() == [120, 120, e[2]]
         assert np.array_equal(codes(c)[~lost], want[~lost]) and (codes(c)[lost] & 0x7F == 0x7F).all(), name
     assert np.array_equal(np.isfinite(f64(p)), ~lost)
+
+
+@pytest.mark.parametrize("betas", [(1 - 1e-9, 1 - 1e-12), (1 - 2.0 ** -53, 1 - 2.0 ** -53), (1 - 1e-6, 1 - 1e-8),
+                                   (0.0, 1 - 1e-10), (0.999999, 0.0)])
+@pytest.mark.parametrize("taken", [0, 1, 12345])
+def test_factors_next_to_one(moe, betas, taken):
+    """The corrections 1 - beta^t are good to float32 for every beta below 1 and every step."""
+    announce(f"adamw betas={betas} after {taken} steps")
+    n = 1000
+    g = torch.randn(n, generator=gen(33), device="cuda")
+    p = torch.randn(n, generator=gen(34), device="cuda")
+    opt = moe.AdamW([p], lr=LR, betas=betas, eps=EPS, weight_decay=0.0)
+    opt.counter[0] = taken
+    # the moments that as many steps of unit gradients would have left, so that a move is about lr
+    for t, b in ((opt.m[0], betas[0]), (opt.v[0], betas[1])):
+        t.fill_(-np.expm1(taken * np.log(b)) if b and taken else 0.0)
+    before, m, v = f64(p), f64(opt.m[0]), f64(opt.v[0])
+    opt.step([g])
+    torch.cuda.synchronize()
+    want = to.adamw(before, f64(g), m, v, taken + 1, LR, *betas, EPS, 0.0)[0]
+    move = np.abs(want - before)
+    assert np.isfinite(want).all() and move.max() > 0.1 * LR
+    # a move from roots and reciprocals of a unit each, float32 moments and four roundings; the parameter rounded twice
+    assert_within("param", f64(p), want, 2.0 ** -20 * move + 2 * U32 * (np.abs(want) + np.abs(before)))
