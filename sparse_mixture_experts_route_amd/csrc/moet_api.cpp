@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <new>
 
 #include "../../include/moe_train.h"
 #include "api_common.h"
@@ -204,9 +205,28 @@ struct Span {
   bool out;
 };
 
+// (Those of a long list on the heap: they are 24 bytes each, up to seven a tensor, and
+// a thread's stack may be small.)
 struct Spans {
-  Span s[MOET_MAX_TENSORS * 7 + 8];
+  static constexpr int kFew = 16 * 7 + 8;
+  Span few[kFew];
+  Span* s = few;
   int n = 0;
+  Spans() = default;
+  Spans(const Spans&) = delete;
+  Spans& operator=(const Spans&) = delete;
+  ~Spans() {
+    if (s != few) delete[] s;
+  }
+  // Room for a list's tensors and what goes with them; false: no memory
+  bool reserve(int32_t tensors) {
+    if (tensors * 7 + 8 > kFew) {
+      Span* const many = new (std::nothrow) Span[tensors * 7 + 8];
+      if (!many) return false;
+      s = many;
+    }
+    return true;
+  }
   bool add(const void* p, size_t bytes, bool out) {
     const uintptr_t a = (uintptr_t)p;
     if (!p || !aligned16(p) || bytes > UINTPTR_MAX - a) return false;
@@ -256,6 +276,7 @@ moe_status_t check_step(const moet_tensor_t* tensors, int32_t count, const moet_
   const int64_t total = list_values(tensors, count);
   if (total == -1) return MOE_ERR_INVALID_ARGUMENT;
   if (total == -2) return MOE_ERR_UNSUPPORTED;
+  if (!spans.reserve(count)) return MOE_ERR_HIP;
   bool ok = spans.add(counter, 8, true) && (!lr_scale || spans.add(lr_scale, 4, false));
   for (int i = 0; ok && i < count; ++i) {
     const moet_tensor_t& t = tensors[i];
@@ -339,6 +360,7 @@ MOE_API moe_status_t moet_grad_norm(const moet_tensor_t* tensors, int32_t count,
   if (total == -1) return MOE_ERR_INVALID_ARGUMENT;
   if (total == -2) return MOE_ERR_UNSUPPORTED;
   Spans spans;
+  if (!spans.reserve(count)) return MOE_ERR_HIP;
   bool ok = spans.add(norm, 4, true) && (!scale || spans.add(scale, 4, true)) &&
             spans.add(ws, MOET_GRAD_NORM_WS_BYTES, true);
   for (int i = 0; ok && i < count; ++i)
