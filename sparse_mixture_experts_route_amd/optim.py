@@ -7,6 +7,7 @@ from typing import Optional, Sequence
 import torch
 
 from . import _ext, _train
+from ._lib import MOE_DTYPE_BF16, MOE_DTYPE_F32
 from .layer import _torch_stream
 
 _KINDS = ("master", "m", "m_scale", "v", "v_scale")
@@ -25,6 +26,9 @@ class AdamW:
     A step only enqueues work: it can be captured into a graph. It reads lr when it
     is enqueued, and at every replay `lr_scale`, a float32 tensor of this object
     that a schedule may write; the number of steps is kept on the GPU (`counter`).
+
+    The parameters are updated where they were when the object was made; a step
+    refuses one that has been given other memory since (as `p.data = q` does).
 
     state: buffers to go on from, lists by the names master, m, m_scale, v, v_scale
     (None where a parameter has none) and counter, as `state` gives them; they are
@@ -62,7 +66,7 @@ class AdamW:
         if missing or any(len(state[k]) != n for k in _KINDS):
             raise ValueError(f"state needs lists of {n} for {', '.join(_KINDS)}, and a counter")
         for k in _KINDS:
-            setattr(self, k, list(state[k]))
+            setattr(self, k, tuple(state[k]))  # the list below has their addresses
         self.counter = state["counter"]
         self._list = (_train.Tensor * n)()
         for i, (d, f) in enumerate(zip(each(weight_decay, "weight_decay"), each(lr_factor, "lr_factor"))):
@@ -71,6 +75,9 @@ class AdamW:
             self._list[i] = _train.tensor_entry(self.params[i], None, self.master[i], self.m[i], self.m_scale[i],
                                                 self.v[i], self.v_scale[i], float(f), float(d))
         self._entries = list(self._list)  # each entry's own view of the array
+        self._held = [t for k in _KINDS for t in getattr(self, k) if t is not None]
+        self._places = [p.data_ptr() for p in self.params]
+        self._sizes = [p.numel() for p in self.params]
         self._options = _train.AdamWOptions()
         with torch.cuda.device(self.device):
             self.lr_scale = torch.ones(1, device=self.device)
@@ -88,9 +95,8 @@ class AdamW:
         if handle not in self._known:
             self._known.add(handle)
             s = _torch_stream(self.device, stream)
-            for t in (self.counter, self.lr_scale, self.norm, self.scale, self._ws, *(t for k in _KINDS for t in getattr(self, k))):
-                if t is not None:
-                    t.record_stream(s)
+            for t in (self.counter, self.lr_scale, self.norm, self.scale, self._ws, *self._held):
+                t.record_stream(s)
 
     def _fresh(self, width):
         s = {k: [] for k in _KINDS}
@@ -116,10 +122,13 @@ class AdamW:
         gradients before clipping (this object's buffer), None without max_norm."""
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
+        if list(map(torch.Tensor.data_ptr, self.params)) != self._places:
+            raise RuntimeError("a parameter's memory is not the one that this object was made with")
         self._keep(stream)
         dev = self.device.index
-        for e, g in zip(self._entries, grads):
-            _train.set_grad(e, g, dev)
+        for e, n, g in zip(self._entries, self._sizes, grads):  # _train.set_grad's, without reading n from the entry
+            e.grad = _ext._ptr("grad", g, n, _train._EITHER, dev)
+            e.grad_dtype = MOE_DTYPE_BF16 if g.dtype == torch.bfloat16 else MOE_DTYPE_F32
         opt, clip = self._options, self.max_norm is not None
         opt.lr, (opt.beta1, opt.beta2), opt.eps, opt.seed = self.lr, self.betas, self.eps, self.seed & 0xFFFFFFFF
         if not clip:
