@@ -12,6 +12,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_FILE = os.path.join(_HERE, "libmoe.so")
 
 MOE_OK = 0
+MOE_ERR_INVALID_ARGUMENT = 1
 MOE_DTYPE_F32 = 0
 MOE_DTYPE_BF16 = 1
 MOE_STAGE_PERMUTE = 0

@@ -2,12 +2,13 @@
 
 from __future__ import annotations
 
+import math
 from typing import Optional, Sequence
 
 import torch
 
 from . import _ext, _train
-from ._lib import MOE_DTYPE_BF16, MOE_DTYPE_F32
+from ._lib import MOE_DTYPE_BF16, MOE_DTYPE_F32, MOE_ERR_INVALID_ARGUMENT, MoEError
 from .layer import _torch_stream
 
 _KINDS = ("master", "m", "m_scale", "v", "v_scale")
@@ -72,6 +73,10 @@ class AdamW:
         for i, (d, f) in enumerate(zip(each(weight_decay, "weight_decay"), each(lr_factor, "lr_factor"))):
             if self.params[i].get_device() != self.device.index:
                 raise ValueError(f"parameter {i} is on {self.params[i].device}, the first on {self.device}")
+            if not (0 <= f < math.inf and 0 <= d < math.inf):
+                raise ValueError(f"parameter {i} has lr_factor {f} and weight_decay {d}, expected finite numbers from 0 on")
+            if any(t is not None and t.data_ptr() % 16 for t in (self.params[i], *(getattr(self, k)[i] for k in _KINDS))):
+                raise MoEError(MOE_ERR_INVALID_ARGUMENT, f"AdamW: parameter {i} or its state is not aligned to 16 bytes")
             self._list[i] = _train.tensor_entry(self.params[i], None, self.master[i], self.m[i], self.m_scale[i],
                                                 self.v[i], self.v_scale[i], float(f), float(d))
         self._entries = list(self._list)  # each entry's own view of the array
