@@ -26,7 +26,8 @@ typedef enum {
   MOET_STAGE_LINEAR_BACKWARD = 2  /* moet_linear_backward */
 } moet_stage_t;
 
-/* Workspace bytes that `stage` needs for problem `p` (host only, nothing is enqueued). */
+/* Workspace bytes that `stage` needs for problem `p` (host only, nothing is enqueued).
+ * Any valid problem has a size, also one that the entry point itself does not support. */
 moe_status_t moet_workspace_size(const moe_problem_t* p, int32_t stage, size_t* bytes);
 
 /* ---- Rows sorted by expert and back, with weights, and the gradients.
@@ -94,7 +95,8 @@ moe_status_t moet_gate_backward(const moe_problem_t* p, const float* logits, con
  *   bfloat16; u [T, N] bfloat16 or NULL: u rounded, which the backward pass takes
  * y is made from u before it is rounded. Sums are float32. T, K, N are used; the
  * other fields must form a valid problem. bf16 problems only; MOE_ERR_UNSUPPORTED
- * also when x, W or the rows of y reach 2 GiB.
+ * also when x, W or the rows of y reach 2 GiB, or K or N 2^22 (256 rows of either
+ * are reached with one 32-bit offset). moet_linear_backward has the same limits.
  *   ws at least moet_workspace_size(p, MOET_STAGE_LINEAR) bytes */
 typedef enum {
   MOET_ACT_NONE = 0,
