@@ -20,7 +20,8 @@ the kernels' own work and schedule, so the constants are a least-squares fit:
   permute   b0 + b1 * [one-workgroup form, T <= 1024] + b2 * [separate
             scan launch, more than 64 blocks of 256 tokens] + b3 * M
             selections (index arrays only: the token rows reach the first
-            GEMM through perm)
+            GEMM through perm) + b4 * thousands of experts (the counts that
+            every block clears, adds over the blocks and scans)
   ffn       f0 * launches (each GEMM, and its fixup unless split tiles are
             completed inside the launch or K is too short to split) + f1 * K
             steps of 64 run by the busiest persistent block of a matrix-core
@@ -254,7 +255,7 @@ def features(s: Sample) -> Dict[str, np.ndarray]:
     g2 = _gemm_terms(s.counts, de, d, E, False)
     return {
         "route": np.array([1.0, chain, chain * ep / 64, (ns * E / 1e3) if ns > 1 else 0.0, R / 1e6]),
-        "permute": np.array([1.0, small, scan_launch, R / 1e6]),
+        "permute": np.array([1.0, small, scan_launch, R / 1e6, E / 1e3]),
         "ffn": np.array([2.0 + g1["fixup"] + g2["fixup"], g1["steps"] + g2["steps"], g1["tiles"] + g2["tiles"],
                          g1["partial_mb"] + g2["partial_mb"], g1["stream_steps"] + g2["stream_steps"],
                          g1["stream_mb"] + g2["stream_mb"]]),
