@@ -305,10 +305,14 @@ __global__ __launch_bounds__(kThreads) void from_rows_kernel(const u32x4* __rest
 
 // Index and rows of a few selections in one launch: workgroup (t, part) counts the
 // selections before its token's own ones in the order of the rows, P compares for
-// each, and writes its part of their rows; one more workgroup counts the experts.
-// Against histograms, ranks and rows in three launches, us in a graph: 32 tokens of 8
-// selections 5.6 / 11.9, 512 of 8 14.4 / 18.6, 1024 of 2 9.9 / 11.7, 1024 of 4 14.6 / 14.6,
-// 2048 of 2 22.5 / 11.9.
+// each, and writes its part of their rows; one more workgroup counts the experts. The
+// compares are made for every part of a row, so their number is T^2 k times the parts.
+// Against histograms, ranks and rows in three launches, us in a graph, rows of one part
+// (bfloat16 of 2048): 32 tokens of 8 selections 4.5 / 10.9, 128 of 8 6.4 / 11.6, 777 of 3
+// 11.1 / 11.9, 1024 of 2 9.8 / 11.5, 512 of 8 15.1 / 15.0; of two (bfloat16 of 7168): 128 of 8
+// 8.0 / 13.2, 1024 of 1 12.3 / 15.5, 777 of 3 20.4 / 16.9, 512 of 8 22.8 / 21.7; of four
+// (float32 of 7168): 128 of 8 11.1 / 16.4, 1024 of 1 19.4 / 20.2, 777 of 3 30.1 / 23.1, 512
+// of 8 40.6 / 31.5.
 constexpr int kSmallPart = 2 * kThreads;  // 16-byte pieces of a row per workgroup
 
 template <bool BF16>
@@ -494,7 +498,8 @@ unsigned grid_of(int64_t waves) { return (unsigned)min(ceil_div(waves, (int64_t)
 
 // (Rows of up to 2^24 values: their parts lie along the grid's second dimension.)
 bool dispatch_small(const moe_problem_t& p) {
-  return p.T <= 1024 && p.T * p.T * p.k <= (int64_t)1 << 21 && p.d_model <= 1 << 24;
+  const int64_t parts = ceil_div(p.d_model / (p.dtype == MOE_DTYPE_BF16 ? 8 : 4), kSmallPart);
+  return p.T <= 1024 && p.T * p.T * p.k * parts <= (int64_t)1 << 21 && p.d_model <= 1 << 24;
 }
 
 hipError_t launch_dispatch_small(const moe_problem_t& p, const int32_t* idx, const float* w, const void* x,
