@@ -130,10 +130,10 @@ class AdamW:
         if list(map(torch.Tensor.data_ptr, self.params)) != self._places:
             raise RuntimeError("a parameter's memory is not the one that this object was made with")
         self._keep(stream)
-        dev = self.device.index
+        dev, ptr, either, bf16 = self.device.index, _ext._ptr, _train._EITHER, torch.bfloat16
         for e, n, g in zip(self._entries, self._sizes, grads):  # _train.set_grad's, without reading n from the entry
-            e.grad = _ext._ptr("grad", g, n, _train._EITHER, dev)
-            e.grad_dtype = MOE_DTYPE_BF16 if g.dtype == torch.bfloat16 else MOE_DTYPE_F32
+            e.grad = ptr("grad", g, n, either, dev)
+            e.grad_dtype = MOE_DTYPE_BF16 if g.dtype is bf16 else MOE_DTYPE_F32
         opt, clip = self._options, self.max_norm is not None
         opt.lr, (opt.beta1, opt.beta2), opt.eps, opt.seed = self.lr, self.betas, self.eps, self.seed & 0xFFFFFFFF
         if not clip:
