@@ -21,9 +21,9 @@
 // later stage are issued between the matrix instructions. Workgroups are
 // persistent: while a tile's results leave, the first stages of the next come in, and
 // its first step waits for neither (waiting for the stores there: 8192 x 2048 -> 8192
-// 331 us with u, 287 and 269 for the gradients, then 291, 234 and 235; now 271, 225 and
-// 230: 1014 to 1222 TFLOP/s where torch's products alone reach 1215, 1153 and 943. Other
-// places of the barrier, of the reads and of the loads among the matrix instructions, and
+// 331 us with u, 287 and 269 for the gradients, then 291, 234 and 235; now 271 to 285, 225 and
+// 230: 964 to 1222 TFLOP/s where torch's products alone reach 1215, 1153 and 943; traced
+// between other kernels 307, 227 and 229. Other places of the barrier, of the reads and of the loads among the matrix instructions, and
 // priorities, make no difference).
 // The results go through LDS of their own as float32 rows, so that bias, activation and
 // residual are applied in 16-byte pieces of the row and rounded once.
@@ -389,8 +389,10 @@ __global__ __launch_bounds__(WM * WN * 64, OCC * WM * WN / 4) void dense_kernel(
               for (int z = 0; z < 4; ++z) f[4 * v + z] = w[z] + bias[4 * v + z];
             }
             const int at = inside ? (int)(off * 2) : 0x7FFFFFF0;
-            // u passes by the caches: the backward pass reads it, later than they keep it
-            // (8192 x 2048 -> 8192 with u 296 -> 271 us)
+            // u passes by the caches: the backward pass reads it, later than they keep it. By / through,
+            // forward with u, and with the gradients right after: 512 x 2048 -> 2048 (2 MB) 23 / 23 and
+            // 59 / 59 us, 2048 x 2048 -> 4096 (17 MB) 40 / 41 and 139 / 139, 4096 x 2048 -> 8192 (67 MB)
+            // 132 / 134 and 448 / 448, 8192 x 2048 -> 8192 (134 MB) 274 / 293 and 809 / 818
             if (E.u) __builtin_amdgcn_raw_buffer_store_b128(narrow8(f), rsU, at, 0, 2);
             act_all<8>(f, E.act);
             if (E.residual) {
@@ -572,9 +574,13 @@ __global__ __launch_bounds__(256) void dense_join_kernel(const float* __restrict
 }
 
 // dU = dy act'(u), and sums of its columns: 256 columns by `rows` rows a workgroup, 8
-// columns a thread and 8 rows beside each other. 8192 x 8192: 102 us for 403 MB, behind a
-// product whose 268 MB of results leave the last-level cache meanwhile (2048 columns a
-// workgroup, 4 KB of a row at a time: 106).
+// columns a thread and 8 rows beside each other. 8192 x 8192: 85 us for 403 MB, 4.7 TB/s
+// (when it was 102, 2048 columns a workgroup, 4 KB of a row at a time, took 106). dy and u
+// are loaded past the caches, which leaves dU there for the products: 8192 x 1024 -> 4096 with
+// gradients 276 us, through them 295; 8192 x 2048 -> 8192 809 and 825; up to 34 MB of u equal.
+// dU is rounded to bfloat16, as the products' operands are (two bfloat16 parts of it would
+// make each product twice): dx and dW are then off by 0.0023 of themselves in the norm, the
+// rounding of dU and their own being 0.0017 each. The sums of its columns are of dU before.
 constexpr int kSlopeCols = 256;
 template <int ACT>
 __global__ __launch_bounds__(256) void slope_kernel(const bf16_bits* __restrict__ dy, const bf16_bits* __restrict__ u,

@@ -12,9 +12,10 @@
 // The moments are updated in 64 bits, where a CU multiplies as fast as in
 // 32: their codes then do not depend on how the two products are rounded.
 //
-// Measured: 67 million values, moments in 32 bits 358 us (5.2 TB/s), in 8 bits 205 us
-// (5.2 TB/s), their norm 28 us;
-// 525 thousand values in 5 tensors 6.7 us, a step with its norm 11 us.
+// Measured in a graph: 67 million values, moments in 32 bits 361 us (5.2 TB/s), in 8 bits
+// 209 us (5.1 TB/s), with their norm 386 and 233; 525 thousand values in 5 tensors 6.8 us,
+// with their norm 11. (Traced one by one, behind other kernels: 368 and 228, the norm 35 to
+// 40 and at best 27, its 134 MB at 5 TB/s.)
 #include "common.h"
 #include "e4m3.h"
 #include "internal.h"
@@ -39,6 +40,9 @@ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
 // whose gradients are at most 192 MB. Step with norm, NT / through the caches, 32-bit
 // moments and 8-bit ones: 4 M values (through) 34 and 26 us, 8 M 54 / 58 and 39 / 43, 67 M
 // 404 / 409 and 247 / 259, 134 M 850 / 817 and 511 / 512, 268 M 1720 / 1631 and 1031 / 1031.
+// The step alone, whose gradients a kernel has just written (with that kernel): 8 M 54 / 59 and
+// 37 / 42, 16 M 110 / 109 and 72 / 75, 67 M 438 / 430 and 272 / 278; not just written: 8 M 48 /
+// 52 and 32 / 34, 16 M 92 / 98 and 58 / 62, 67 M 402 / 380 and 231 / 227.
 template <bool NT, typename V>
 __device__ __forceinline__ V load(const V* p) {
   return NT ? __builtin_nontemporal_load(p) : *p;

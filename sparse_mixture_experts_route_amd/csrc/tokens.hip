@@ -483,13 +483,23 @@ __global__ __launch_bounds__(kThreads) void gate_backward_kernel(const float* __
 
 constexpr int64_t kMostBlocks = 1 << 22;  // the rest by strides: a launch holds less than 2^32 threads
 
-// Arrays of 128 MB or more pass by the caches
+// Arrays of 128 MB or more pass by the caches. By / through, us in a graph, arrays that change
+// from call to call, 8 selections, bfloat16 rows of 2048: 4096 tokens (134 MB) dispatch 37 / 38,
+// combine 27 / 30, combine's gradient with dots 63 / 69, dispatch's 33 / 36; 7000 tokens 57 / 64,
+// 46 / 50, 100 / 108, 54 / 60; 12000 tokens 88 / 101, 77 / 89, 160 / 174, 88 / 100; below, 2048
+// tokens (67 MB), 25 / 24, 15 / 15, 39 / 31. (Combine right behind the dispatch of the same rows
+// would want them through: 64 / 62 and 102 / 95, from 10000 tokens on 139 / 175; the experts'
+// products come between.)
 bool streams(const moe_problem_t& p) {
   return (double)p.T * p.k * p.d_model * (p.dtype == MOE_DTYPE_BF16 ? 2 : 4) >= (double)(128 << 20);
 }
 
 // Waves of a token whose dot products are wanted: one where the tokens fill the chip or
-// a row is one step of a wave
+// a row is one step of a wave. One / four, us in a graph, gradient of combine and of dispatch,
+// 8 selections of bfloat16 rows of 2048: 64 tokens 8.1 / 5.6 and 7.1 / 5.5, 512 11.6 / 10.1 and
+// 9.2 / 8.0, 1024 16.3 / 14.2 and 11.8 / 13.4, 2048 28.9 / 27.7 and 16.7 / 21.3, 3000 42 / 40
+// and 27 / 31; rows of 7168: 512 29 / 24 and 21 / 16, 4000 187 / 186 and 111 / 103; 2 selections
+// of rows of 1024 (one step): 1024 tokens 5.5 / 7.5 and 4.9 / 9.3.
 int dot_waves(const moe_problem_t& p, int64_t row_vecs) { return p.T >= 2048 || row_vecs <= kStep ? 1 : kWaves; }
 
 unsigned grid_of(int64_t waves) { return (unsigned)min(ceil_div(waves, (int64_t)kWaves), kMostBlocks); }
