@@ -23,8 +23,8 @@
 // its first step waits for neither (waiting for the stores there: 8192 x 2048 -> 8192
 // 331 us with u, 287 and 269 for the gradients, then 291, 234 and 235; now 271 to 285, 225 and
 // 230: 964 to 1222 TFLOP/s where torch's products alone reach 1215, 1153 and 943; traced
-// between other kernels 307, 227 and 229. Other places of the barrier, of the reads and of the loads among the matrix instructions, and
-// priorities, make no difference).
+// between other kernels 307, 227 and 229. Other places of the barrier, of the reads and of
+// the loads among the matrix instructions, and priorities, make no difference).
 // The results go through LDS of their own as float32 rows, so that bias, activation and
 // residual are applied in 16-byte pieces of the row and rounded once.
 //

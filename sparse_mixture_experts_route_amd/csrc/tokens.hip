@@ -487,7 +487,7 @@ constexpr int64_t kMostBlocks = 1 << 22;  // the rest by strides: a launch holds
 // from call to call, 8 selections, bfloat16 rows of 2048: 4096 tokens (134 MB) dispatch 37 / 38,
 // combine 27 / 30, combine's gradient with dots 63 / 69, dispatch's 33 / 36; 7000 tokens 57 / 64,
 // 46 / 50, 100 / 108, 54 / 60; 12000 tokens 88 / 101, 77 / 89, 160 / 174, 88 / 100; below, 2048
-// tokens (67 MB), 25 / 24, 15 / 15, 39 / 31. (Combine right behind the dispatch of the same rows
+// tokens (67 MB, one array for all results) 25 / 24, 15 / 15, 39 / 31. (Combine right behind the dispatch of the same rows
 // would want them through: 64 / 62 and 102 / 95, from 10000 tokens on 139 / 175; the experts'
 // products come between.)
 bool streams(const moe_problem_t& p) {

@@ -75,10 +75,10 @@ class AdamW:
                 raise ValueError(f"parameter {i} is on {self.params[i].device}, the first on {self.device}")
             if not (0 <= f < math.inf and 0 <= d < math.inf):
                 raise ValueError(f"parameter {i} has lr_factor {f} and weight_decay {d}, expected finite numbers from 0 on")
-            if any(t is not None and t.data_ptr() % 16 for t in (self.params[i], *(getattr(self, k)[i] for k in _KINDS))):
-                raise MoEError(MOE_ERR_INVALID_ARGUMENT, f"AdamW: parameter {i} or its state is not aligned to 16 bytes")
             self._list[i] = _train.tensor_entry(self.params[i], None, self.master[i], self.m[i], self.m_scale[i],
                                                 self.v[i], self.v_scale[i], float(f), float(d))
+            if any((getattr(self._list[i], k) or 0) % 16 for k in ("param", *_KINDS)):
+                raise MoEError(MOE_ERR_INVALID_ARGUMENT, f"AdamW: parameter {i} or its state is not aligned to 16 bytes")
         self._entries = list(self._list)  # each entry's own view of the array
         self._held = [t for k in _KINDS for t in getattr(self, k) if t is not None]
         self._places = [p.data_ptr() for p in self.params]

@@ -34,3 +34,16 @@ def test_alignment(moe):
     assert opt.counter.tolist() == [0, 0]
     with pytest.raises(ValueError, match="expected 512"):
         moe.AdamW(params, state={**state, "v": [state["v"][0], wide]})
+
+
+def test_state_that_is_no_tensor(moe):
+    params, _ = params_of([(304, F32, F32), (512, BF, BF)], 53)
+    state = moe.AdamW(params).state
+    for name in ("m", "v"):
+        for bad in ([0.0] * 304, 1.0):
+            with pytest.raises(TypeError, match=f"{name} must be a torch.Tensor"):
+                moe.AdamW(params, state={**state, name: [bad, state[name][1]]})
+        with pytest.raises(ValueError, match=f"{name} is required"):
+            moe.AdamW(params, state={**state, name: [None, state[name][1]]})
+        with pytest.raises(ValueError, match="GPU"):
+            moe.AdamW(params, state={**state, name: [state[name][0].cpu(), state[name][1]]})
